@@ -15,6 +15,9 @@ import re
 
 import torch
 
+from . import moe
+from .moe import *  # noqa: F401,F403 - the mixture-of-experts operators (include/fp8blk_moe.h)
+
 __all__ = [
     "FP8_BLOCK_1x32_E8M0", "FP8_BLOCK_1x128_F32", "FP8_BLOCK_128x128_F32",
     "FP8_E8M0_CEIL", "FP8_E8M0_FLOOR", "FP8_OUT_BF16", "FP8_OUT_F32",
@@ -27,7 +30,7 @@ __all__ = [
     "quantize", "dequantize", "fake_quant_merge", "block_scaled_gemm", "grouped_gemm", "lora_backward", "nvfp4_quantize", "nvfp4_dequantize",
     "scale_shape",
     "is_routed_expert_weight", "quantize_state_dict",
-]
+] + moe.__all__
 
 FP8_OK = 0
 FP8_BLOCK_1x32_E8M0, FP8_BLOCK_1x128_F32, FP8_BLOCK_128x128_F32 = 0, 1, 2
@@ -95,6 +98,7 @@ def library():
         lib.fp8_abi_version.restype = ci
         if lib.fp8_abi_version() != ABI_VERSION:
             raise ImportError("libfp8blk.so ABI version mismatch")
+        moe.declare(lib)
         _lib = lib
     return _lib
 

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libfp8blk.so")
 
-SOURCES = ["quantize.hip", "dequant.hip", "merge.hip", "gemm.hip", "lora_bwd.hip", "nvfp4.hip", "abi.cpp"]
+SOURCES = ["quantize.hip", "dequant.hip", "merge.hip", "gemm.hip", "lora_bwd.hip", "nvfp4.hip", "rmsnorm.hip", "route.hip",
+           "matvec.hip", "combine.hip", "abi.cpp", "abi_moe.cpp"]
 
 # -ffp-contract=off: every fused multiply-add in the kernels is written out
 # explicitly, so rounding follows the source exactly.  Packed fp32 vector

@@ -8,22 +8,17 @@
 #include <mutex>
 #include <string.h>
 
+#include "host.h"
 #include "launch.h"
 
+namespace fp8blk {
+
 namespace {
-
 constexpr int kMaxDevices = 64;
-
-struct DeviceInfo {
-  bool ok = false;
-  bool supported = false;
-  int num_cu = 0;
-};
-
 DeviceInfo g_dev[kMaxDevices];
 std::once_flag g_once[kMaxDevices];
+}  // namespace
 
-// Properties of the current device, read once per device.
 int current_device(DeviceInfo** out) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return FP8_ERR_HIP;
@@ -41,10 +36,11 @@ int current_device(DeviceInfo** out) {
   return FP8_OK;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+}  // namespace fp8blk
 
-// a * b <= lim for non-negative a, b, without overflowing int64.
-bool product_at_most(int64_t a, int64_t b, int64_t lim) { return b == 0 || a <= lim / b; }
+namespace {
+
+using namespace fp8blk;
 
 // Element counts beyond 2^60 are rejected before any size arithmetic.
 constexpr int64_t kMaxElements = int64_t(1) << 60;
@@ -53,8 +49,6 @@ static_assert(FP8BLK_NOALLOC_SCRATCH_BYTES == (unsigned long long)fp8blk::kLoraS
 
 // GEMM reductions: per-tile A/B offsets are 32-bit (256 rows x K bytes).
 constexpr int64_t kMaxGemmK = int64_t(1) << 24;
-
-int hip_status(hipError_t e) { return e == hipSuccess ? FP8_OK : FP8_ERR_HIP; }
 
 bool valid_kind(int k) { return k == FP8_BLOCK_1x32_E8M0 || k == FP8_BLOCK_1x128_F32 || k == FP8_BLOCK_128x128_F32; }
 

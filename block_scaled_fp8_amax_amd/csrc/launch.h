@@ -68,4 +68,99 @@ hipError_t launch_nvfp4_quant(const uint16_t* x, int64_t rows, int64_t cols, int
 hipError_t launch_nvfp4_dequant(const uint8_t* q, const uint8_t* bs, const float* gs, int64_t rows, int64_t cols,
                                 int64_t rpt, uint16_t* x, hipStream_t stream);
 
+// ------------------------------------------------ mixture-of-experts operators
+
+// Workgroups of a launch at most (a launch's threads have to stay below
+// 2^32); kernels that take one row or token per workgroup walk on from there.
+constexpr int64_t kMaxGrid = int64_t(1) << 20;
+
+struct RmsNorm {
+  const uint16_t* x;
+  const uint16_t* residual;
+  const void* weight;
+  bool weight_f32;
+  int64_t rows, cols;
+  float eps;
+  int blk;            // 32 or 128
+  bool floor_rule;
+  uint8_t* q;
+  void* scale;
+  uint16_t *h, *y, *ydq;
+  float* rstd;
+};
+hipError_t launch_rmsnorm_quant(const RmsNorm& a, hipStream_t stream);
+// Partial weight gradients the backward pass keeps: [parts][cols] floats.
+int64_t rmsnorm_bwd_parts(int64_t rows);
+hipError_t launch_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const void* w, bool w_f32, const float* rstd,
+                              const uint16_t* dres, int64_t rows, int64_t cols, void* workspace, uint16_t* dx,
+                              void* dw, hipStream_t stream);
+
+struct RouteArgs {
+  const void* logits;
+  const float* bias;
+  int64_t tokens;
+  int experts, top_k, groups, topk_groups;
+  int score, group_score, renorm, logits_f32;
+  float scale;
+  int32_t* ids;
+  float* weights;
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
+struct RouteBwdArgs {
+  const void* logits;
+  const int32_t* ids;
+  const float* dweights;
+  int64_t tokens;
+  int experts, top_k, score, renorm, logits_f32;
+  float scale;
+  void* dlogits;
+};
+hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t stream);
+int64_t plan_workspace_bytes(int64_t pairs, int experts);
+hipError_t launch_plan(const int32_t* ids, int64_t tokens, int top_k, int experts, void* workspace, int32_t* offsets,
+                       int32_t* row_index, int32_t* slot, hipStream_t stream);
+
+struct MatvecArgs {
+  const uint16_t* x;
+  int64_t x_rows;
+  const int32_t* row_index;   // null = the row itself
+  const uint8_t* q;
+  const uint8_t* block_scale;
+  const float* global_scale;
+  int64_t rows_per_tensor;
+  const int32_t* offsets;     // null = one group of all rows
+  int64_t groups, total_m, n, k;
+  void* y;
+  bool out_f32;
+};
+hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream);
+
+struct CombineArgs {
+  const void* rows;
+  int64_t total_m;
+  const int32_t* slot;
+  const float* weights;
+  const uint16_t* residual;
+  int64_t tokens;
+  int top_k;
+  int64_t n;
+  void* y;
+  bool row_f32, out_f32;
+};
+hipError_t launch_combine(const CombineArgs& a, hipStream_t stream);
+struct CombineBwdArgs {
+  const void* dy;
+  const void* rows;
+  int64_t total_m;
+  const int32_t* slot;
+  const float* weights;
+  int64_t tokens;
+  int top_k;
+  int64_t n;
+  void* drows;
+  float* dweights;
+  bool dy_f32, row_f32;
+};
+hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream);
+
 }  // namespace fp8blk

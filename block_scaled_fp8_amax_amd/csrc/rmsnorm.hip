@@ -1,0 +1,380 @@
+// Residual addition, root-mean-square norm and FP8 quantization of the
+// normed rows (gfx950), and the norm's backward pass.
+//
+//   h = RN_bf16(x + r);  rstd = 1 / sqrt(mean h^2 + eps);  y = h rstd w
+//   1x128: s = RN32(amax|y| / 448), code = e4m3(RN32(y / s))
+//   1x32 : X from amax|y| by the E8M0 rule, code = e4m3(y 2^-X)
+// y stays in fp32 between the norm and the FP8 rounding (rounding it to bf16
+// first would round twice); h is rounded to bf16 because it is the residual
+// stream that the next layer and the backward pass read.
+//
+// One workgroup per row.  Thread t holds the 8-element chunks t, t + T, ...
+// of the row in registers between the sum of squares and the encode, so the
+// row is read once; a 1x128 tile is 16 adjacent lanes, a 1x32 block 4.
+#include "device.h"
+#include "launch.h"
+
+namespace fp8blk {
+
+namespace {
+
+__device__ __forceinline__ float group_add64(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+// Sum over the workgroup (its waves' sums added in wave order, so the
+// result does not depend on timing); red holds 16 floats.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = group_add64(v);
+  const int waves = (int)(blockDim.x >> 6);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int i = 0; i < waves; ++i) s += red[i];
+  __syncthreads();
+  return s;
+}
+
+__device__ __forceinline__ void unpack8(const u32x4& v, float* f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf_lo(w[i]);
+    f[2 * i + 1] = bf_hi(w[i]);
+  }
+}
+
+__device__ __forceinline__ u32x4 pack8(const float* f) {
+  return (u32x4){pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+}
+
+// Weights of chunk c as fp32.
+template <bool WF32>
+__device__ __forceinline__ void load_weight8(const void* w, int c, float* f) {
+  if constexpr (WF32) {
+    const v4f* p = reinterpret_cast<const v4f*>(w) + 2 * c;
+    const v4f a = p[0], b = p[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = a[i];
+      f[4 + i] = b[i];
+    }
+  } else {
+    unpack8(reinterpret_cast<const u32x4*>(w)[c], f);
+  }
+}
+
+struct NormParams {
+  const u32x4* x;
+  const u32x4* res;
+  const void* w;
+  int nch;          // chunks per row
+  float cols;
+  float eps;
+  u32x2* q;
+  void* scale;
+  u32x4* h;
+  u32x4* y;
+  u32x4* ydq;
+  float* rstd;
+  int64_t rows;
+};
+
+// E8M0 code of a block from its fp32 amax: as e8m0_code, on the fp32 bits.
+// CEIL: X is the smallest integer with amax <= 1.75 * 2^(8 + X), so one is
+// added where the mantissa is above 1.75 (0x600000).
+template <bool FLOOR>
+__device__ __forceinline__ uint32_t e8m0_code_f32(uint32_t bits) {
+  int c = (int)(bits >> 23) - 8;
+  if (!FLOOR) c += (bits & 0x7FFFFFu) > 0x600000u ? 1 : 0;
+  c = c < 0 ? 0 : c;
+  return (uint32_t)(c > 254 ? 254 : c);
+}
+
+// BLK 32 or 128; CH chunks per thread.
+template <int BLK, bool FLOOR, bool WF32, int CH>
+__global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormParams p) {
+  __shared__ float red[16];
+  const int T = (int)blockDim.x, t = (int)threadIdx.x;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+  const int64_t base = row * p.nch;
+  float f[CH][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = t + i * T;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (c < p.nch) {
+      v = p.x[base + c];
+      if (p.res) {
+        float a[8], b[8];
+        unpack8(v, a);
+        unpack8(p.res[base + c], b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] += b[j];
+        v = pack8(a);
+        p.h[base + c] = v;
+      }
+    }
+    unpack8(v, f[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(f[i][j], f[i][j], ss);
+  }
+  ss = block_sum(ss, red);
+  float rstd = 1.0f / sqrtf(ss / p.cols + p.eps);
+  if (!(ss < __builtin_inff())) {
+    // squares left the fp32 range: the same with h 2^-64 (uniform branch)
+    float s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = f[i][j] * 0x1p-64f;
+        s2 = __builtin_fmaf(d, d, s2);
+      }
+    s2 = block_sum(s2, red);
+    rstd = 0x1p-64f / sqrtf(s2 / p.cols + p.eps * 0x1p-128f);
+  }
+  if (p.rstd && t == 0) p.rstd[row] = rstd;
+
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = t + i * T;
+    const bool in = c < p.nch;
+    float w[8];
+    load_weight8<WF32>(p.w, in ? c : 0, w);
+    float am = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[i][j] = f[i][j] * rstd * w[j];
+      am = __builtin_fmaxf(am, __builtin_fabsf(f[i][j]));
+    }
+    // chunks past the row are whole tiles past it: their lanes take part in
+    // the lane reductions with zeros and store nothing
+    const uint32_t bits = group_max<BLK / 8>(in ? __float_as_uint(am) : 0u);
+    float v[8], sval;
+    uint32_t code = 0;
+    if constexpr (BLK == 128) {
+      const float amax = __uint_as_float(bits);
+      sval = amax / kE4M3Max;
+      // tiny tiles are scaled by 2^64 so that the reciprocal stays finite
+      const float pre = amax < 0x1p-60f ? 0x1p64f : 1.0f;
+      const float sp = sval * pre;
+      const float r = sval > 0.f ? 1.0f / sp : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float yp = f[i][j] * pre;
+        const float q0 = yp * r;
+        const float rn = __builtin_fmaf(q0, sp, -yp);
+        v[j] = clamp448(__builtin_fmaf(rn, -r, q0));
+      }
+    } else {
+      code = e8m0_code_f32<FLOOR>(bits);
+      sval = e8m0_val(code);
+      // 2^-X in two factors: X reaches 120 for y near the fp32 maximum
+      const int X = (int)code - 127;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = clamp448(__builtin_ldexpf(f[i][j], -X));
+    }
+    if (in) {
+      u32x2 cc;
+      cc.x = cvt4_e4m3(v[0], v[1], v[2], v[3]);
+      cc.y = cvt4_e4m3(v[4], v[5], v[6], v[7]);
+      p.q[base + c] = cc;
+      if (p.y) p.y[base + c] = pack8(f[i]);
+      if (p.ydq) {
+        float d[8];
+        decode4_e4m3(cc.x, d);
+        decode4_e4m3(cc.y, d + 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] *= sval;
+        p.ydq[base + c] = pack8(d);
+      }
+      if ((t & (BLK / 8 - 1)) == 0) {
+        if constexpr (BLK == 128)
+          reinterpret_cast<float*>(p.scale)[(base + c) / 16] = sval;
+        else
+          reinterpret_cast<uint8_t*>(p.scale)[(base + c) / 4] = (uint8_t)code;
+      }
+    }
+  }
+  }
+}
+
+struct NormBwdParams {
+  const u32x4* dy;
+  const u32x4* h;
+  const void* w;
+  const float* rstd;
+  const u32x4* dres;
+  int64_t rows;
+  int nch;
+  float cols;
+  u32x4* dx;
+  float* part;      // [grid][cols] partial weight gradients
+};
+
+// Workgroup b takes the rows b, b + G, ...; the weight gradient of its rows
+// stays in registers and goes to the workspace once.
+template <bool WF32, int CH>
+__global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
+  __shared__ float red[16];
+  const int T = (int)blockDim.x, t = (int)threadIdx.x;
+  float acc[CH][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t base = row * p.nch;
+    const float rstd = p.rstd[row];
+    float xh[CH][8], wd[CH][8];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + i * T;
+      const bool in = c < p.nch;
+      u32x4 a = {0u, 0u, 0u, 0u}, b = {0u, 0u, 0u, 0u};
+      if (in) {
+        a = p.h[base + c];
+        b = p.dy[base + c];
+      }
+      float w[8];
+      load_weight8<WF32>(p.w, in ? c : 0, w);
+      unpack8(a, xh[i]);
+      unpack8(b, wd[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        xh[i][j] *= rstd;
+        acc[i][j] = __builtin_fmaf(wd[i][j], xh[i][j], acc[i][j]);
+        wd[i][j] *= w[j];
+        dot = __builtin_fmaf(wd[i][j], xh[i][j], dot);
+      }
+    }
+    const float c1 = block_sum(dot, red) / p.cols;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + i * T;
+      if (c >= p.nch) continue;
+      float d[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = rstd * __builtin_fmaf(-xh[i][j], c1, wd[i][j]);
+      if (p.dres) {
+        float r[8];
+        unpack8(p.dres[base + c], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] += r[j];
+      }
+      p.dx[base + c] = pack8(d);
+    }
+  }
+  v4f* out = reinterpret_cast<v4f*>(p.part) + (int64_t)blockIdx.x * p.nch * 2;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = t + i * T;
+    if (c >= p.nch) continue;
+    out[2 * c] = (v4f){acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+    out[2 * c + 1] = (v4f){acc[i][4], acc[i][5], acc[i][6], acc[i][7]};
+  }
+}
+
+// Sum of the partial weight gradients: 64 columns per workgroup, its four
+// waves take the partials in turn and are added in wave order.
+template <bool WF32>
+__global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* __restrict__ part, int parts, int cols,
+                                                         void* __restrict__ dw) {
+  __shared__ float red[4][64];
+  const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+  const int col = (int)blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (col < cols)
+    for (int i = wave; i < parts; i += 4) s += part[(int64_t)i * cols + col];
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && col < cols) {
+    s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    if constexpr (WF32)
+      reinterpret_cast<float*>(dw)[col] = s;
+    else
+      reinterpret_cast<uint16_t*>(dw)[col] = (uint16_t)pack_bf16x2(s, 0.f);
+  }
+}
+
+// Chunks per thread and threads for a row of nch chunks.
+void row_shape(int nch, int* ch, int* threads) {
+  *ch = nch <= 1024 ? 1 : nch <= 2048 ? 2 : 4;
+  *threads = ((nch + *ch - 1) / *ch + 63) / 64 * 64;
+}
+
+constexpr int kMaxParts = 512;
+
+}  // namespace
+
+int64_t rmsnorm_bwd_parts(int64_t rows) { return rows < kMaxParts ? rows : kMaxParts; }
+
+hipError_t launch_rmsnorm_quant(const RmsNorm& a, hipStream_t stream) {
+  const int nch = (int)(a.cols / 8);
+  int ch, threads;
+  row_shape(nch, &ch, &threads);
+  NormParams p{reinterpret_cast<const u32x4*>(a.x), reinterpret_cast<const u32x4*>(a.residual), a.weight, nch,
+               (float)a.cols, a.eps, reinterpret_cast<u32x2*>(a.q), a.scale, reinterpret_cast<u32x4*>(a.h),
+               reinterpret_cast<u32x4*>(a.y), reinterpret_cast<u32x4*>(a.ydq), a.rstd, a.rows};
+  const dim3 grid((unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid)), block((unsigned)threads);
+#define FP8BLK_NORM(B, F, W, C) \
+  hipLaunchKernelGGL((rmsnorm_quant_kernel<B, F, W, C>), grid, block, 0, stream, p)
+#define FP8BLK_NORM_CH(B, F, W)                     \
+  do {                                              \
+    if (ch == 1) FP8BLK_NORM(B, F, W, 1);           \
+    else if (ch == 2) FP8BLK_NORM(B, F, W, 2);      \
+    else FP8BLK_NORM(B, F, W, 4);                   \
+  } while (0)
+#define FP8BLK_NORM_W(B, F)                         \
+  do {                                              \
+    if (a.weight_f32) FP8BLK_NORM_CH(B, F, true);   \
+    else FP8BLK_NORM_CH(B, F, false);               \
+  } while (0)
+  if (a.blk == 128) FP8BLK_NORM_W(128, false);
+  else if (a.floor_rule) FP8BLK_NORM_W(32, true);
+  else FP8BLK_NORM_W(32, false);
+#undef FP8BLK_NORM_W
+#undef FP8BLK_NORM_CH
+#undef FP8BLK_NORM
+  return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const void* w, bool w_f32, const float* rstd,
+                              const uint16_t* dres, int64_t rows, int64_t cols, void* workspace, uint16_t* dx,
+                              void* dw, hipStream_t stream) {
+  const int nch = (int)(cols / 8);
+  const int parts = (int)rmsnorm_bwd_parts(rows);
+  float* part = reinterpret_cast<float*>(workspace);
+  if (rows > 0) {
+    int ch, threads;
+    row_shape(nch, &ch, &threads);
+    NormBwdParams p{reinterpret_cast<const u32x4*>(dy), reinterpret_cast<const u32x4*>(h), w, rstd,
+                    reinterpret_cast<const u32x4*>(dres), rows, nch, (float)cols,
+                    reinterpret_cast<u32x4*>(dx), part};
+    const dim3 grid((unsigned)parts), block((unsigned)threads);
+#define FP8BLK_NB(W, C) hipLaunchKernelGGL((rmsnorm_bwd_kernel<W, C>), grid, block, 0, stream, p)
+    if (w_f32) {
+      if (ch == 1) FP8BLK_NB(true, 1);
+      else if (ch == 2) FP8BLK_NB(true, 2);
+      else FP8BLK_NB(true, 4);
+    } else {
+      if (ch == 1) FP8BLK_NB(false, 1);
+      else if (ch == 2) FP8BLK_NB(false, 2);
+      else FP8BLK_NB(false, 4);
+    }
+#undef FP8BLK_NB
+  }
+  const dim3 grid((unsigned)((cols + 63) / 64));
+  if (w_f32)
+    hipLaunchKernelGGL(rmsnorm_dw_kernel<true>, grid, dim3(256), 0, stream, part, parts, (int)cols, dw);
+  else
+    hipLaunchKernelGGL(rmsnorm_dw_kernel<false>, grid, dim3(256), 0, stream, part, parts, (int)cols, dw);
+  return hipGetLastError();
+}
+
+}  // namespace fp8blk

@@ -32,10 +32,11 @@ Modules
   gemm    block-scaled GEMM and grouped GEMM references, error metric
   lora_grad  QAT backward for the LoRA factors (straight-through fake-quant)
   nvfp4   NVFP4 prequant: E2M1 codes, e4m3 1x16 block scales, per-tensor fp32 scale
+  moe     norm, routing, plan, combination and NVFP4 products around the experts
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against closed forms, brute force, torch's own dtype casts or exact
 rational arithmetic; none is "parity unpinned".
 """
 
-from . import codec, quant, merge, gemm, lora_grad, nvfp4  # noqa: F401
+from . import codec, quant, merge, gemm, lora_grad, nvfp4, moe  # noqa: F401

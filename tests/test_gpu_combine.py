@@ -1,0 +1,115 @@
+"""GPU parity of fp8_moe_combine / fp8_moe_combine_backward against the oracle (oracle/moe.py, float64).
+
+An fp32 sum of k weighted rows and a residual is off by at most (k + 1) 2^-24 of the terms' magnitudes, a bf16 output
+adds 2^-8 of the value; drows is one product (2^-24, or 2^-8 in bf16); a dot product over n columns in fp32 is off
+by at most n 2^-24 of the magnitudes in any order.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_fp8_amax_amd as fb
+from oracle import moe
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _t(a, dtype):
+    return torch.from_numpy(np.asarray(a, dtype=np.float32)).to(dtype).cuda()
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _slots(rng, tokens, top_k, total):
+    s = rng.permutation(max(total, tokens * top_k))[: tokens * top_k].reshape(tokens, top_k).astype(np.int32)
+    s[s >= total] = -1
+    return s
+
+
+SHAPES = [(1, 1, 8, 1), (1, 8, 7168, 8), (5, 2, 40, 12), (33, 8, 256, 200), (3, 64, 1024, 192), (2, 3, 32768, 6),
+          (7, 4, 2056, 0), (260, 6, 128, 1560)]
+
+
+@pytest.mark.parametrize("tokens,top_k,n,total", SHAPES)
+@pytest.mark.parametrize("row_dtype", [BF, F32])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("residual", [False, True])
+def test_combine(tokens, top_k, n, total, row_dtype, out_dtype, residual):
+    print(f"[combine] {tokens} tokens, {top_k} of {total} rows of {n}, {row_dtype} {out_dtype} res={residual}",
+          flush=True)
+    rng = np.random.default_rng(tokens + n)
+    rows = _t(rng.standard_normal((total, n)), row_dtype)
+    slot, w = _slots(rng, tokens, top_k, total), rng.uniform(-1, 1, (tokens, top_k)).astype(np.float32)
+    res = _t(4 * rng.standard_normal((tokens, n)), BF) if residual else None
+    y = torch.full((tokens, n), 9.0, dtype=out_dtype, device="cuda")
+    fb.fp8_moe_combine(rows, torch.from_numpy(slot).cuda(), torch.from_numpy(w).cuda(), y, residual=res)
+    r64, s64 = _np(rows), None if res is None else _np(res)
+    want = moe.combine(r64, slot, w, s64)
+    mag = moe.combine(np.abs(r64), slot, np.abs(w), None if s64 is None else np.abs(s64))
+    tol = (top_k + 1) * 2.0 ** -24 * mag + (2.0 ** -8 * np.abs(want) if out_dtype == BF else 0)
+    assert np.all(np.abs(_np(y) - want) <= tol)
+
+
+def test_combine_over_the_residual_and_of_left_out_pairs():
+    rng = np.random.default_rng(3)
+    rows = _t(rng.standard_normal((6, 64)), BF)
+    rows[5] = float("nan")                                       # a row no slot names
+    slot = np.array([[0, 1], [-1, -1], [6, 2], [np.iinfo(np.int32).min, np.iinfo(np.int32).max]], dtype=np.int32)
+    w = np.array([[1, 2], [np.nan, np.inf], [np.nan, 0.5], [np.nan, np.nan]], dtype=np.float32)
+    res = _t(rng.standard_normal((4, 64)), BF)
+    keep = res.clone()
+    fb.fp8_moe_combine(rows, torch.from_numpy(slot).cuda(), torch.from_numpy(w).cuda(), res, residual=res)
+    assert torch.equal(res[1], keep[1]) and torch.equal(res[3], keep[3])
+    want = moe.combine(_np(rows[:5]), np.where(slot < 5, slot, -1), np.nan_to_num(w), _np(keep))
+    assert np.all(np.abs(_np(res) - want) <= 2.0 ** -7 * np.abs(want) + 2.0 ** -20)
+
+
+def test_same_row_for_two_tokens():
+    """Reading a row twice is fine (a row shared by tokens)."""
+    rows = _t(np.arange(32).reshape(2, 16), BF)
+    slot = torch.tensor([[1, 1], [1, 0]], dtype=torch.int32, device="cuda")
+    y = fb.moe_combine(rows, slot, torch.ones((2, 2), device="cuda"), out_dtype=F32)
+    assert torch.equal(y, torch.stack([2 * rows[1].float(), rows[0].float() + rows[1].float()]))
+
+
+@pytest.mark.parametrize("tokens,top_k,n,total", SHAPES)
+@pytest.mark.parametrize("row_dtype", [BF, F32])
+@pytest.mark.parametrize("dy_dtype", [BF, F32])
+def test_backward(tokens, top_k, n, total, row_dtype, dy_dtype):
+    """Rows that no slot names keep what they held; pairs left out get a weight gradient of 0."""
+    print(f"[combine backward] {tokens} tokens, {top_k} of {total} rows of {n}, {row_dtype} {dy_dtype}", flush=True)
+    rng = np.random.default_rng(tokens + n + 1)
+    rows, dy = _t(rng.standard_normal((total, n)), row_dtype), _t(rng.standard_normal((tokens, n)), dy_dtype)
+    slot, w = _slots(rng, tokens, top_k, total), rng.uniform(-1, 1, (tokens, top_k)).astype(np.float32)
+    if total > 3:
+        slot[slot == 3] = -1
+    drows = torch.full_like(rows, 7.0)
+    dw = torch.full((tokens, top_k), 9.0, dtype=F32, device="cuda")
+    fb.fp8_moe_combine_backward(dy, rows, torch.from_numpy(slot).cuda(), torch.from_numpy(w).cuda(), drows, dw)
+    d64, r64 = _np(dy), _np(rows)
+    want, wantw = moe.combine_backward(d64, r64, slot, w, np.full((total, n), 7.0))
+    step = 2.0 ** -8 if row_dtype == BF else 2.0 ** -24
+    assert np.all(np.abs(_np(drows) - want) <= step * np.abs(want))
+    _, mag = moe.combine_backward(np.abs(d64), np.abs(r64), slot, w, np.zeros((total, n)))
+    assert np.all(np.abs(_np(dw) - wantw) <= n * 2.0 ** -24 * mag)
+    assert np.all(_np(dw)[slot < 0] == 0)
+
+
+def test_backward_against_differences():
+    """The combination is linear: its difference along a direction is the gradient's product with it."""
+    rng = np.random.default_rng(5)
+    rows, dy = _t(rng.standard_normal((12, 64)), F32), _t(rng.standard_normal((4, 64)), F32)
+    slot = torch.from_numpy(_slots(rng, 4, 3, 12)).cuda()
+    w = _t(rng.uniform(0, 1, (4, 3)), F32)
+    drows, dw = fb.moe_combine_backward(dy, rows, slot, w)
+    v, u = _t(rng.standard_normal((12, 64)), F32), _t(rng.standard_normal((4, 3)), F32)
+    for moved, grad, args in ((v, drows, [(rows + v, w), (rows - v, w)]), (u, dw, [(rows, w + u), (rows, w - u)])):
+        up, dn = (_np(fb.moe_combine(r, slot, ww, out_dtype=F32)) for r, ww in args)
+        got = (_np(dy) * (up - dn)).sum() / 2
+        want = (_np(moved) * _np(grad)).sum()
+        mag = (np.abs(_np(dy)) * (np.abs(up) + np.abs(dn))).sum() + (np.abs(_np(moved) * _np(grad))).sum()
+        assert abs(got - want) <= 64 * 2.0 ** -24 * mag
