@@ -43,10 +43,14 @@ int combine_args(int row_type, int other_type, int64_t total_m, int64_t tokens, 
   return FP8_OK;
 }
 
-int matvec_shape(int64_t rows_per_tensor, int64_t m, int64_t n, int64_t k, int y_type) {
+// x is read with 32-bit byte offsets.
+constexpr int64_t kMaxMatvecX = (int64_t(1) << 30) - 1;
+
+int matvec_shape(int64_t x_rows, int64_t rows_per_tensor, int64_t m, int64_t n, int64_t k, int y_type) {
   if (!valid_type(y_type)) return FP8_ERR_INVALID_ARG;
   if (m < 0 || m > kMaxRows || n < 0 || n > kMaxWidth || k <= 0 || k > kMaxWidth || k % 16) return FP8_ERR_SHAPE;
   if (rows_per_tensor < 1 || n % rows_per_tensor) return FP8_ERR_SHAPE;
+  if (x_rows < 0 || !product_at_most(x_rows, k, kMaxMatvecX)) return FP8_ERR_SHAPE;
   return FP8_OK;
 }
 
@@ -167,7 +171,7 @@ int fp8_moe_plan(const int32_t* ids, int64_t tokens, int top_k, int experts, voi
 
 int fp8_nvfp4_matvec(const uint16_t* x, const uint8_t* q, const uint8_t* block_scale, const float* global_scale,
                      int64_t rows_per_tensor, int64_t m, int64_t n, int64_t k, void* y, int y_type, void* stream) {
-  if (int s = matvec_shape(rows_per_tensor, m, n, k, y_type)) return s;
+  if (int s = matvec_shape(m, rows_per_tensor, m, n, k, y_type)) return s;
   if (m == 0 || n == 0) return FP8_OK;
   if (!x || !q || !block_scale || !global_scale || !y) return FP8_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(q, 8) || !aligned(global_scale, 4) || !aligned(y, type_bytes(y_type)))
@@ -183,9 +187,8 @@ int fp8_nvfp4_grouped_matvec(const uint16_t* x, int64_t x_rows, const int32_t* r
                              const uint8_t* block_scale, const float* global_scale, int64_t rows_per_tensor,
                              const int32_t* group_offsets, int64_t groups, int64_t total_m, int64_t n, int64_t k,
                              void* y, int y_type, void* stream) {
-  if (int s = matvec_shape(rows_per_tensor, total_m, n, k, y_type)) return s;
+  if (int s = matvec_shape(x_rows, rows_per_tensor, total_m, n, k, y_type)) return s;
   if (groups < 1 || groups > 1024) return FP8_ERR_INVALID_ARG;
-  if (x_rows < 0 || x_rows > kMaxRows) return FP8_ERR_SHAPE;
   if (total_m == 0 || n == 0) return FP8_OK;
   if (x_rows == 0 || (!row_index && x_rows != total_m)) return FP8_ERR_SHAPE;
   if (!x || !q || !block_scale || !global_scale || !group_offsets || !y) return FP8_ERR_INVALID_ARG;

@@ -96,13 +96,18 @@ def _bad(where, name, t, dtypes, shape, dev):
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be contiguous")
-    raise ValueError(f"{where}: tensors on different devices ({dev} and {t.device} for {name})")
+    raise ValueError(f"{where}: tensors on different devices ({_device(dev)} and {t.device} for {name})")
+
+
+def _device(dev):
+    return torch.device("cuda", dev) if dev >= 0 else torch.device("cpu")
 
 
 def _need(where, name, t, dtypes, shape, dev):
-    """The address of a contiguous tensor of one of ``dtypes`` and exactly ``shape`` on ``dev``."""
+    """The address of a contiguous tensor of one of ``dtypes`` and exactly
+    ``shape`` on GPU number ``dev`` (-1: the host, which _run refuses)."""
     try:
-        if t.shape == shape and t.dtype in dtypes and t.device == dev and t.is_contiguous():
+        if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -125,21 +130,28 @@ def _workspace(where, t, dev):
     """(address, bytes) of a workspace tensor of any type; None where none is needed."""
     if t is None:
         return None, 0
-    if not isinstance(t, torch.Tensor) or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{where}: the workspace must be a contiguous tensor on {dev}")
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{where}: the workspace must be a contiguous tensor on {_device(dev)}")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+# torch's current stream of a GPU as a raw handle.  The public call builds a
+# Stream object first, 1.9 of the 8.7 us of a small call; torch's own
+# compiled code takes the handle directly too.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _run(where, dev, stream, fn, *args):
-    """Calls an entry point on ``stream`` (None: torch's current one) with ``dev`` as the current device, which is
-    the one the library launches on."""
-    if dev.type != "cuda":
-        raise ValueError(f"{where}: every tensor must be on a GPU, got {dev}")
+    """Calls an entry point on ``stream`` (None: torch's current one) with GPU number ``dev`` as the current device,
+    which is the one the library launches on."""
+    if dev < 0:
+        raise ValueError(f"{where}: every tensor must be on a GPU")
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
+        handle = _raw_stream(dev)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev.index == torch.cuda.current_device():
+    if dev == torch.cuda.current_device():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -179,7 +191,7 @@ def fp8_rmsnorm_quantize(x, weight, eps, kind, rule, q, scale, residual=None, h=
     block = _choice(where, "kind", kind, _BLOCKS)
     shape = _dims(where, "x", x, 2)
     rows, cols = shape
-    dev = x.device
+    dev = x.get_device()
     px = _need(where, "x", x, (_BF,), shape, dev)
     pw = _need(where, "weight", weight, _FLOATS, (cols,), dev)
     pq = _need(where, "q", q, _CODES, shape, dev)
@@ -213,7 +225,7 @@ def fp8_rmsnorm_backward(dy, h, weight, rstd, workspace, dx, dweight, dres=None,
     where = "fp8_rmsnorm_backward"
     shape = _dims(where, "dy", dy, 2)
     rows, cols = shape
-    dev = dy.device
+    dev = dy.get_device()
     pdy = _need(where, "dy", dy, (_BF,), shape, dev)
     pw = _need(where, "weight", weight, _FLOATS, (cols,), dev)
     ws, ws_bytes = _workspace(where, workspace, dev)
@@ -239,7 +251,7 @@ def fp8_moe_route(logits, ids, weights, bias=None, score="softmax", groups=1, to
     where = "fp8_moe_route"
     tokens, experts = _dims(where, "logits", logits, 2)
     shape = _dims(where, "ids", ids, 2)
-    dev = logits.device
+    dev = logits.get_device()
     pl = _need(where, "logits", logits, _FLOATS, (tokens, experts), dev)
     if shape[0] != tokens:
         raise ValueError(f"{where}: ids has shape {tuple(shape)}, expected ({tokens}, top_k)")
@@ -258,7 +270,7 @@ def fp8_moe_route_backward(logits, ids, dweights, dlogits, score="softmax", reno
     where = "fp8_moe_route_backward"
     tokens, experts = _dims(where, "logits", logits, 2)
     shape = _dims(where, "ids", ids, 2)
-    dev = logits.device
+    dev = logits.get_device()
     pl = _need(where, "logits", logits, _FLOATS, (tokens, experts), dev)
     if shape[0] != tokens:
         raise ValueError(f"{where}: ids has shape {tuple(shape)}, expected ({tokens}, top_k)")
@@ -287,7 +299,7 @@ def fp8_moe_plan(ids, experts, workspace, offsets, row_index, slot, stream=None)
     where = "fp8_moe_plan"
     shape = _dims(where, "ids", ids, 2)
     tokens, top_k = shape
-    dev = ids.device
+    dev = ids.get_device()
     ws, ws_bytes = _workspace(where, workspace, dev)
     _run(where, dev, stream, _lib().fp8_moe_plan, _need(where, "ids", ids, (_I32,), shape, dev), tokens, top_k, experts,
          ws, ws_bytes, _need(where, "offsets", offsets, (_I32,), (experts + 1,), dev),
@@ -303,7 +315,7 @@ def fp8_nvfp4_matvec(x, q, block_scale, global_scale, rows_per_tensor, y, stream
     where = "fp8_nvfp4_matvec"
     m, k = _dims(where, "x", x, 2)
     n = _dims(where, "q", q, 2)[0]
-    dev = x.device
+    dev = x.get_device()
     if rows_per_tensor < 1 or n % rows_per_tensor:
         raise ValueError(f"{where}: rows_per_tensor {rows_per_tensor} does not divide n {n}")
     _run(where, dev, stream, _lib().fp8_nvfp4_matvec, _need(where, "x", x, (_BF,), (m, k), dev),
@@ -325,7 +337,7 @@ def fp8_nvfp4_grouped_matvec(x, row_index, q, block_scale, global_scale, rows_pe
     x_rows, k = _dims(where, "x", x, 2)
     groups, n, _ = _dims(where, "q", q, 3)
     total_m = _dims(where, "y", y, 2)[0]
-    dev = x.device
+    dev = x.get_device()
     if rows_per_tensor < 1 or n % rows_per_tensor:
         raise ValueError(f"{where}: rows_per_tensor {rows_per_tensor} does not divide n {n}")
     if row_index is None and x_rows != total_m:
@@ -347,7 +359,7 @@ def fp8_moe_combine(rows, slot, weights, y, residual=None, stream=None):
     where = "fp8_moe_combine"
     total_m, n = _dims(where, "rows", rows, 2)
     shape = _dims(where, "slot", slot, 2)
-    dev = rows.device
+    dev = rows.get_device()
     out = (shape[0], n)
     _run(where, dev, stream, _lib().fp8_moe_combine, _need(where, "rows", rows, _FLOATS, (total_m, n), dev),
          _is_f32(rows), total_m, _need(where, "slot", slot, (_I32,), shape, dev),
@@ -363,7 +375,7 @@ def fp8_moe_combine_backward(dy, rows, slot, weights, drows, dweights, stream=No
     where = "fp8_moe_combine_backward"
     total_m, n = _dims(where, "rows", rows, 2)
     shape = _dims(where, "slot", slot, 2)
-    dev = rows.device
+    dev = rows.get_device()
     _run(where, dev, stream, _lib().fp8_moe_combine_backward,
          _need(where, "dy", dy, _FLOATS, (shape[0], n), dev), _is_f32(dy),
          _need(where, "rows", rows, _FLOATS, (total_m, n), dev), _is_f32(rows), total_m,

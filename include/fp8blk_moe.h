@@ -181,8 +181,8 @@ int fp8_moe_plan_workspace(int64_t tokens, int top_k, int experts, size_t* bytes
  * fp8_nvfp4_quantize (q 8-byte aligned); y [m x n] out, bf16 or float per
  * y_type (aligned to its element).
  * Shape: 0 <= m < 2^31, 0 <= n <= 2^24, rows_per_tensor >= 1, n %
- *        rows_per_tensor == 0, k % 16 == 0, 0 < k <= 2^24; m == 0 or n == 0
- *        enqueues nothing.
+ *        rows_per_tensor == 0, k % 16 == 0, 0 < k <= 2^24, m * k < 2^30;
+ *        m == 0 or n == 0 enqueues nothing.
  */
 int fp8_nvfp4_matvec(const uint16_t* x, const uint8_t* q, const uint8_t* block_scale, const float* global_scale,
                      int64_t rows_per_tensor, int64_t m, int64_t n, int64_t k, void* y, int y_type, void* stream);
@@ -198,7 +198,8 @@ int fp8_nvfp4_matvec(const uint16_t* x, const uint8_t* q, const uint8_t* block_s
  * host, with offsets clamped into [0, total_m] and indices into [0, x_rows).
  * Rows of y at or behind off[groups] are left as they were.
  * Shape: 1 <= groups <= 1024, 0 <= total_m < 2^31, x_rows >= 1 where there
- *        are rows (x_rows == total_m without row_index); n, k as above.
+ *        are rows (x_rows == total_m without row_index), x_rows * k < 2^30;
+ *        n, k as above.
  */
 int fp8_nvfp4_grouped_matvec(const uint16_t* x, int64_t x_rows, const int32_t* row_index, const uint8_t* q,
                              const uint8_t* block_scale, const float* global_scale, int64_t rows_per_tensor,

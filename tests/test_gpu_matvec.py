@@ -73,6 +73,20 @@ def test_random(m, n, k, dtype):
     assert np.all(np.abs(_out(y) - want) <= tol)
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 4112, 320), (2, 5000, 192), (9, 5008, 192), (20, 5008, 208), (2, 16400, 64),
+                                   (1, 16401, 576), (30, 16400, 128), (12, 16400, 80), (16, 16401, 64), (2, 16400, 48),
+                                   (50, 300, 1024), (31, 4097, 272)])
+def test_exact_on_larger_grids(m, n, k):
+    """Row and tile counts on both sides of every choice of launch shape."""
+    print(f"[matvec] larger grid {m}x{n}x{k}", flush=True)
+    rng = np.random.default_rng(m + n + k)
+    x = rng.integers(-8, 9, (m, k)).astype(np.float64)
+    q, bs = _grid_matrix(rng, n, k)
+    y = fb.nvfp4_matvec(bf16_from_bits(f32_to_bf16(x.astype(np.float32))), torch.from_numpy(q).cuda(),
+                        torch.from_numpy(bs).cuda(), torch.ones(1, device="cuda"), out_dtype=torch.float32)
+    assert np.array_equal(_out(y), x @ moe.nvfp4_matrix(q, bs, [1.0], n).T)
+
+
 def test_stacked_tensor_scales_and_every_code():
     """Each run of rows_per_tensor rows has its own scale; every code byte under every e4m3 scale byte but NaN."""
     q = np.repeat(np.arange(256, dtype=np.uint8)[:, None], 16, axis=1)             # k = 32
@@ -106,7 +120,11 @@ def test_codes_at_an_eight_byte_offset():
 
 
 GROUPS = [([3, 0, 2, 1], 96, 512), ([0, 0, 0], 16, 64), ([1] * 9, 33, 128), ([40, 1, 0, 17], 48, 272),
-          ([0, 5], 64, 2048), ([8], 20, 1024), ([0] * 30 + [2] + [0] * 40 + [1], 24, 96)]
+          ([0, 5], 64, 2048), ([8], 20, 1024), ([0] * 30 + [2] + [0] * 40 + [1], 24, 96),
+          # large grids: at most two rows on average (with a group of many among them), some, many; odd k
+          ([1, 2, 0, 1, 20, 1, 1, 0, 3, 1, 2, 1, 2, 1, 0, 2] * 2, 560, 192), ([1] * 40, 420, 1088),
+          ([5, 1, 17, 0, 8], 4000, 128), ([33, 1, 40, 0, 21], 4000, 64), ([2, 1, 1, 2], 4400, 80),
+          ([0] * 300 + [1, 2, 3] + [0] * 300, 6000, 64), ([1] * 1024, 16, 32)]
 
 
 @pytest.mark.parametrize("sizes,n,k", GROUPS)
