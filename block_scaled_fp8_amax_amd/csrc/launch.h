@@ -104,6 +104,8 @@ struct RouteArgs {
   float scale;
   int32_t* ids;
   float* weights;
+  int per = 0, log_width = 0;   // experts per group, log2 of lanes per group (set by the launcher)
+  float inv_per = 0.f;
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 struct RouteBwdArgs {

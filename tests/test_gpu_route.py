@@ -72,6 +72,27 @@ def test_grouped(score, gs, experts, groups, kept, top_k):
     _check(l, l64, bias, top_k, score, groups, kept, gs)
 
 
+@pytest.mark.parametrize("experts,groups,kept,top_k", [(256, 1, 1, 8), (256, 8, 4, 8), (160, 8, 3, 6), (130, 13, 2, 9),
+                                                       (100, 1, 1, 40), (96, 32, 7, 3), (66, 33, 9, 5)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_many_tokens(experts, groups, kept, top_k, score):
+    """The launch shapes for many tokens choose as those for a few do (which are compared with the oracle)."""
+    tokens = 4101
+    l = 1.5 * torch.randn((tokens, experts), device="cuda", generator=torch.Generator("cuda").manual_seed(experts))
+    l[7] = -float("inf")
+    l[tokens - 1, 1:] = -float("inf")
+    b = 0.1 * torch.randn(experts, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    for bias in (None, b):
+        for gs in ("max", "top2"):
+            kw = dict(bias=bias, score=score, groups=groups, topk_groups=kept, group_score=gs, renorm=True)
+            ids, w = fb.moe_route(l, top_k, **kw)
+            for at in range(0, tokens, 1367):
+                part = slice(at, min(tokens, at + 1367))
+                i2, w2 = fb.moe_route(l[part].contiguous(), top_k, **kw)
+                assert torch.equal(ids[part], i2), (bias is not None, gs, at)
+                assert torch.all((w[part] - w2).abs() <= 2.0 ** -18 * w2.abs())
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_ties_go_to_the_lowest_index(score):
     rng = np.random.default_rng(2)
@@ -204,7 +225,7 @@ def _plan_check(ids, experts):
 
 @pytest.mark.parametrize("tokens,top_k,experts", [(0, 2, 4), (1, 1, 1), (1, 8, 256), (5, 3, 7), (256, 8, 64),
                                                   (257, 8, 256), (1000, 6, 160), (4099, 8, 256), (700, 64, 1024),
-                                                  (131072, 1, 3)])
+                                                  (131072, 1, 3), (2048, 1, 5), (2049, 1, 5), (300000, 1, 130), (35000, 8, 257)])
 @pytest.mark.parametrize("kind", ["spread", "one expert", "left out"])
 def test_plan(tokens, top_k, experts, kind):
     print(f"[plan] {tokens} tokens, top {top_k} of {experts}, {kind}", flush=True)
