@@ -85,7 +85,7 @@ int fp8_rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void
 int fp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes) {
   if (!bytes) return FP8_ERR_INVALID_ARG;
   if (int s = norm_shape(rows, cols, 8)) return s;
-  *bytes = (size_t)(rmsnorm_bwd_parts(rows) * cols * 4);
+  *bytes = (size_t)(rmsnorm_bwd_parts(rows, cols) * cols * 4);
   return FP8_OK;
 }
 
@@ -97,7 +97,7 @@ int fp8_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const void* weig
   if (cols == 0) return FP8_OK;
   if (!weight || !dweight) return FP8_ERR_INVALID_ARG;
   if (rows > 0 && (!dy || !h || !rstd || !dx || !workspace)) return FP8_ERR_INVALID_ARG;
-  if (workspace_bytes < (size_t)(rmsnorm_bwd_parts(rows) * cols * 4)) return FP8_ERR_INVALID_ARG;
+  if (workspace_bytes < (size_t)(rmsnorm_bwd_parts(rows, cols) * cols * 4)) return FP8_ERR_INVALID_ARG;
   if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(rstd, 4) || !aligned(dres, 16) ||
       !aligned(workspace, 256) || !aligned(dx, 16) || !aligned(dweight, type_bytes(weight_type)))
     return FP8_ERR_ALIGN;

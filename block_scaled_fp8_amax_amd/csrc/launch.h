@@ -90,7 +90,7 @@ struct RmsNorm {
 };
 hipError_t launch_rmsnorm_quant(const RmsNorm& a, hipStream_t stream);
 // Partial weight gradients the backward pass keeps: [parts][cols] floats.
-int64_t rmsnorm_bwd_parts(int64_t rows);
+int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols);
 hipError_t launch_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const void* w, bool w_f32, const float* rstd,
                               const uint16_t* dres, int64_t rows, int64_t cols, void* workspace, uint16_t* dx,
                               void* dw, hipStream_t stream);

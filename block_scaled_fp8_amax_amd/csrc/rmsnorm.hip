@@ -217,7 +217,11 @@ struct NormBwdParams {
 };
 
 // Workgroup b takes the rows b, b + G, ...; the weight gradient of its rows
-// stays in registers and goes to the workspace once.
+// stays in registers and goes to the workspace once.  Bound by reading dy, h
+// and dres and writing dx: 8192 x 7168 in 88 us (5.3 TB/s) and 4 us for
+// the partials.  Two rows at a time, rows kept packed across the barrier and
+// dres loaded before it all took registers that cost a workgroup per CU, and
+// 10 to 60% more time.
 template <bool WF32, int CH>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
   __shared__ float red[16];
@@ -280,44 +284,66 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
   }
 }
 
-// Sum of the partial weight gradients: 64 columns per workgroup, its four
-// waves take the partials in turn and are added in wave order.
+// Sum of the partial weight gradients: 16 columns per workgroup, 64 threads
+// to a column (thread q takes the partials q, q + 64, ...), added as a tree.
 template <bool WF32>
-__global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* __restrict__ part, int parts, int cols,
-                                                         void* __restrict__ dw) {
-  __shared__ float red[4][64];
-  const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
-  const int col = (int)blockIdx.x * 64 + lane;
+__global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* __restrict__ part, int parts, int cols,
+                                                          void* __restrict__ dw) {
+  __shared__ float red[64][17];
+  const int lane = (int)(threadIdx.x & 15), q = (int)(threadIdx.x >> 4);
+  const int col = (int)blockIdx.x * 16 + lane;
   float s = 0.f;
   if (col < cols)
-    for (int i = wave; i < parts; i += 4) s += part[(int64_t)i * cols + col];
-  red[wave][lane] = s;
+#pragma unroll 8
+    for (int i = q; i < parts; i += 64) s += part[(int64_t)i * cols + col];
+  red[q][lane] = s;
   __syncthreads();
-  if (wave == 0 && col < cols) {
-    s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
-    if constexpr (WF32)
-      reinterpret_cast<float*>(dw)[col] = s;
-    else
-      reinterpret_cast<uint16_t*>(dw)[col] = (uint16_t)pack_bf16x2(s, 0.f);
+  if (threadIdx.x < 16 * 4) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += red[q * 16 + i][lane];
+    s += __shfl_xor(s, 16, 64);
+    s += __shfl_xor(s, 32, 64);
+    if (q == 0 && col < cols) {
+      if constexpr (WF32)
+        reinterpret_cast<float*>(dw)[col] = s;
+      else
+        reinterpret_cast<uint16_t*>(dw)[col] = (uint16_t)pack_bf16x2(s, 0.f);
+    }
   }
 }
 
-// Chunks per thread and threads for a row of nch chunks.
-void row_shape(int nch, int* ch, int* threads) {
-  *ch = nch <= 1024 ? 1 : nch <= 2048 ? 2 : 4;
+// Chunks per thread and threads for a row of nch chunks: two chunks where
+// there are rows enough to fill the card (16384 x 7168 forward: 186 us
+// against 196 with one), one for a few rows (one row: 4.0 us against 4.3).
+void row_shape(int nch, int64_t rows, int* ch, int* threads) {
+  *ch = nch <= 1024 && (rows < 512 || nch <= 128) ? 1 : nch <= 2048 ? 2 : 4;
   *threads = ((nch + *ch - 1) / *ch + 63) / 64 * 64;
 }
 
-constexpr int kMaxParts = 512;
+// Workgroups of the backward pass: 16 waves per CU, and two workgroups where
+// one has more than eight, so that one's loads run beside the other's
+// barrier (8192 x 7168: 99 us against 118 with one; 4096 x 2048: 20 us with
+// four, 23 with eight).
+int64_t bwd_parts(int64_t rows, int threads, int ch) {
+  const int waves = threads / 64, least = ch == 1 ? 2 : 1;
+  const int per_cu = 16 / waves > least ? 16 / waves : least;
+  const int64_t wgs = 256 * (int64_t)per_cu;
+  return rows < wgs ? rows : wgs;
+}
 
 }  // namespace
 
-int64_t rmsnorm_bwd_parts(int64_t rows) { return rows < kMaxParts ? rows : kMaxParts; }
+int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols) {
+  int ch, threads;
+  row_shape((int)(cols / 8), 0, &ch, &threads);
+  return bwd_parts(rows, threads > 0 ? threads : 64, ch);
+}
 
 hipError_t launch_rmsnorm_quant(const RmsNorm& a, hipStream_t stream) {
   const int nch = (int)(a.cols / 8);
   int ch, threads;
-  row_shape(nch, &ch, &threads);
+  row_shape(nch, a.rows, &ch, &threads);
   NormParams p{reinterpret_cast<const u32x4*>(a.x), reinterpret_cast<const u32x4*>(a.residual), a.weight, nch,
                (float)a.cols, a.eps, reinterpret_cast<u32x2*>(a.q), a.scale, reinterpret_cast<u32x4*>(a.h),
                reinterpret_cast<u32x4*>(a.y), reinterpret_cast<u32x4*>(a.ydq), a.rstd, a.rows};
@@ -348,14 +374,13 @@ hipError_t launch_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const void*
                               const uint16_t* dres, int64_t rows, int64_t cols, void* workspace, uint16_t* dx,
                               void* dw, hipStream_t stream) {
   const int nch = (int)(cols / 8);
-  const int parts = (int)rmsnorm_bwd_parts(rows);
+  const int parts = (int)rmsnorm_bwd_parts(rows, cols);
   float* part = reinterpret_cast<float*>(workspace);
   if (rows > 0) {
     int ch, threads;
-    row_shape(nch, &ch, &threads);
+    row_shape(nch, 0, &ch, &threads);
     NormBwdParams p{reinterpret_cast<const u32x4*>(dy), reinterpret_cast<const u32x4*>(h), w, rstd,
-                    reinterpret_cast<const u32x4*>(dres), rows, nch, (float)cols,
-                    reinterpret_cast<u32x4*>(dx), part};
+                    reinterpret_cast<const u32x4*>(dres), rows, nch, (float)cols, reinterpret_cast<u32x4*>(dx), part};
     const dim3 grid((unsigned)parts), block((unsigned)threads);
 #define FP8BLK_NB(W, C) hipLaunchKernelGGL((rmsnorm_bwd_kernel<W, C>), grid, block, 0, stream, p)
     if (w_f32) {
@@ -369,11 +394,11 @@ hipError_t launch_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const void*
     }
 #undef FP8BLK_NB
   }
-  const dim3 grid((unsigned)((cols + 63) / 64));
+  const dim3 grid((unsigned)((cols + 15) / 16));
   if (w_f32)
-    hipLaunchKernelGGL(rmsnorm_dw_kernel<true>, grid, dim3(256), 0, stream, part, parts, (int)cols, dw);
+    hipLaunchKernelGGL(rmsnorm_dw_kernel<true>, grid, dim3(1024), 0, stream, part, parts, (int)cols, dw);
   else
-    hipLaunchKernelGGL(rmsnorm_dw_kernel<false>, grid, dim3(256), 0, stream, part, parts, (int)cols, dw);
+    hipLaunchKernelGGL(rmsnorm_dw_kernel<false>, grid, dim3(1024), 0, stream, part, parts, (int)cols, dw);
   return hipGetLastError();
 }
 
