@@ -9,123 +9,195 @@ namespace fp8blk {
 
 namespace {
 
-constexpr int kCbThreads = 256;
+constexpr int kBatch = 8;            // choices whose rows are loaded together
+// Threads of a workgroup at most.  Forward, one chunk each: 16384 tokens of
+// eight rows of 7168 take 470 us (5.0 TB/s) with 128, 474 with 64, 493 with
+// 192 and 500 to 520 with 256 to 896.  Backward, a whole token: 4093 such
+// tokens take 206 us (4.8 TB/s) with 512, 207 with 256, 212 with 128.
+constexpr int kCbThreads = 128;
+constexpr int kCbBwdThreads = 512;
 
-// Eight consecutive elements from chunk c of a bf16 or fp32 row.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+
+// Row s of `rows` as a buffer; a slot that takes no part reads as zeros (a
+// buffer of no length), without a branch between the loads of a batch.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t chunk, float* f) {
-  if constexpr (F32) {
-    const v4f a = reinterpret_cast<const v4f*>(p)[2 * chunk], b = reinterpret_cast<const v4f*>(p)[2 * chunk + 1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = a[i];
-      f[4 + i] = b[i];
-    }
-  } else {
-    const u32x4 v = reinterpret_cast<const u32x4*>(p)[chunk];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = bf_lo(w[i]);
-      f[2 * i + 1] = bf_hi(w[i]);
-    }
-  }
+__device__ __forceinline__ Buffer row_buffer(const void* rows, int64_t s, int64_t total_m, int64_t n) {
+  const bool in = s >= 0 && s < total_m;
+  const int64_t at = in ? s * n * (F32 ? 4 : 2) : 0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(reinterpret_cast<const char*>(rows)) + at, 0,
+                                           in ? (uint32_t)(n * (F32 ? 4 : 2)) : 0u, 0x00027000);
 }
 
+// Eight consecutive elements, chunk c of a row; bytes past the row are zeros
+// and stores there are dropped.
 template <bool F32>
-__device__ __forceinline__ void store8(void* p, int64_t chunk, const float* f) {
-  if constexpr (F32) {
-    reinterpret_cast<v4f*>(p)[2 * chunk] = (v4f){f[0], f[1], f[2], f[3]};
-    reinterpret_cast<v4f*>(p)[2 * chunk + 1] = (v4f){f[4], f[5], f[6], f[7]};
-  } else {
-    reinterpret_cast<u32x4*>(p)[chunk] = (u32x4){pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                 pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+struct Chunk {
+  u32x4 v[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(Buffer b, int c) {
+    v[0] = __builtin_amdgcn_raw_buffer_load_b128(b, (uint32_t)c * (F32 ? 32 : 16), 0, 0);
+    if constexpr (F32) v[1] = __builtin_amdgcn_raw_buffer_load_b128(b, (uint32_t)c * 32 + 16, 0, 0);
   }
-}
-
-// One workgroup per token.
-template <bool ROW_F32, bool OUT_F32>
-__global__ __launch_bounds__(kCbThreads) void combine_kernel(CombineArgs a) {
-  const int nch = (int)(a.n / 8);
-  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-  const int32_t* slot = a.slot + t * a.top_k;
-  const float* wt = a.weights + t * a.top_k;
-  for (int c = (int)threadIdx.x; c < nch; c += kCbThreads) {
-    float acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    if (a.residual) load8<false>(a.residual, t * nch + c, acc);
-    for (int j = 0; j < a.top_k; ++j) {
-      const int64_t s = slot[j];
-      if (s < 0 || s >= a.total_m) continue;
-      const float w = wt[j];
-      float r[8];
-      load8<ROW_F32>(a.rows, s * nch + c, r);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w, r[i], acc[i]);
-    }
-    store8<OUT_F32>(a.y, t * nch + c, acc);
+  __device__ __forceinline__ void store(Buffer b, int c) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v[0], b, (uint32_t)c * (F32 ? 32 : 16), 0, 0);
+    if constexpr (F32) __builtin_amdgcn_raw_buffer_store_b128(v[1], b, (uint32_t)c * 32 + 16, 0, 0);
   }
-  }
-}
-
-// One workgroup per token; the choices in turn.
-template <bool DY_F32, bool ROW_F32>
-__global__ __launch_bounds__(kCbThreads) void combine_bwd_kernel(CombineBwdArgs a) {
-  __shared__ float red[kCbThreads / 64];
-  const int nch = (int)(a.n / 8);
-  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x)
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t s = a.slot[t * a.top_k + j];
-    float dot = 0.f;
-    if (s >= 0 && s < a.total_m) {
-      const float w = a.weights[t * a.top_k + j];
-      for (int c = (int)threadIdx.x; c < nch; c += kCbThreads) {
-        float d[8], r[8];
-        load8<DY_F32>(a.dy, t * nch + c, d);
-        load8<ROW_F32>(a.rows, s * nch + c, r);
+  __device__ __forceinline__ void get(float* f) const {
+    if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dot = __builtin_fmaf(d[i], r[i], dot);
-          d[i] *= w;
-        }
-        store8<ROW_F32>(a.drows, s * nch + c, d);
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i >> 2][i & 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf_lo(v[0][i]);
+        f[2 * i + 1] = bf_hi(v[0][i]);
       }
     }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) dot += __shfl_xor(dot, d, 64);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) a.dweights[t * a.top_k + j] = (red[0] + red[1]) + (red[2] + red[3]);
-    __syncthreads();
   }
+  __device__ __forceinline__ void set(const float* f) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = __float_as_uint(f[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[0][i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    }
+  }
+};
+
+// A workgroup takes blockDim chunks of one token; `splits` workgroups make up
+// a token.
+template <bool ROW_F32, bool OUT_F32>
+__global__ __launch_bounds__(kCbThreads) void combine_kernel(CombineArgs a, int splits) {
+  for (int64_t wg = blockIdx.x; wg < a.tokens * splits; wg += gridDim.x) {
+    const int64_t t = wg / splits;
+    const int c = (int)(wg - t * splits) * (int)blockDim.x + (int)threadIdx.x;
+    const int32_t* slot = a.slot + t * a.top_k;
+    const float* wt = a.weights + t * a.top_k;
+    float acc[8];
+    Chunk<false> res;
+    if (a.residual) {
+      res.load(row_buffer<false>(a.residual, t, a.tokens, a.n), c);
+      res.get(acc);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    }
+    for (int j0 = 0; j0 < a.top_k; j0 += kBatch) {
+      Chunk<ROW_F32> r[kBatch];
+      float w[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t s = j0 + j < a.top_k ? slot[j0 + j] : -1;
+        w[j] = s >= 0 && s < a.total_m ? wt[j0 + j] : 0.f;
+        r[j].load(row_buffer<ROW_F32>(a.rows, s, a.total_m, a.n), c);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        float f[8];
+        r[j].get(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w[j], f[i], acc[i]);
+      }
+    }
+    Chunk<OUT_F32> y;
+    y.set(acc);
+    y.store(row_buffer<OUT_F32>(a.y, t, a.tokens, a.n), c);
+  }
+}
+
+// One workgroup per token, kBatch choices at a time: dy is read once for all
+// of them, and their dot products are summed over the workgroup together.
+template <bool DY_F32, bool ROW_F32>
+__global__ __launch_bounds__(kCbBwdThreads) void combine_bwd_kernel(CombineBwdArgs a) {
+  __shared__ float red[kCbBwdThreads / 64][kBatch];
+  const int nch = (int)(a.n / 8), t = (int)threadIdx.x, threads = (int)blockDim.x;
+  for (int64_t tok = blockIdx.x; tok < a.tokens; tok += gridDim.x) {
+    const Buffer dyb = row_buffer<DY_F32>(a.dy, tok, a.tokens, a.n);
+    for (int j0 = 0; j0 < a.top_k; j0 += kBatch) {
+      Buffer rb[kBatch], db[kBatch];
+      float w[kBatch], dot[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t s = j0 + j < a.top_k ? a.slot[tok * a.top_k + j0 + j] : -1;
+        w[j] = s >= 0 && s < a.total_m ? a.weights[tok * a.top_k + j0 + j] : 0.f;
+        rb[j] = row_buffer<ROW_F32>(a.rows, s, a.total_m, a.n);
+        db[j] = row_buffer<ROW_F32>(a.drows, s, a.total_m, a.n);
+        dot[j] = 0.f;
+      }
+      for (int c = t; c < nch; c += threads) {
+        Chunk<DY_F32> dy;
+        Chunk<ROW_F32> r[kBatch];
+        dy.load(dyb, c);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) r[j].load(rb[j], c);
+        float d[8];
+        dy.get(d);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          float f[8], g[8];
+          r[j].get(f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dot[j] = __builtin_fmaf(d[i], f[i], dot[j]);
+            g[i] = w[j] * d[i];
+          }
+          Chunk<ROW_F32> o;
+          o.set(g);
+          o.store(db[j], c);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) dot[j] += __shfl_xor(dot[j], d, 64);
+        if ((t & 63) == 0) red[t >> 6][j] = dot[j];
+      }
+      __syncthreads();
+      if (t < kBatch && j0 + t < a.top_k) {
+        float s = 0.f;
+        for (int v = 0; v < threads / 64; ++v) s += red[v][t];
+        a.dweights[tok * a.top_k + j0 + t] = s;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Whole waves for a row of n, at most `most` threads.
+int block_threads(int64_t n, int most) {
+  const int64_t need = (n / 8 + 63) / 64 * 64;
+  return (int)(need < 64 ? 64 : need < most ? need : most);
 }
 
 }  // namespace
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.tokens < kMaxGrid ? a.tokens : kMaxGrid));
+  const int threads = block_threads(a.n, kCbThreads);
+  const int splits = (int)((a.n / 8 + threads - 1) / threads);
+  const int64_t wgs = a.tokens * splits;
+  const dim3 grid((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid)), block((unsigned)threads);
   if (a.row_f32 && a.out_f32)
-    hipLaunchKernelGGL((combine_kernel<true, true>), grid, dim3(kCbThreads), 0, stream, a);
+    hipLaunchKernelGGL((combine_kernel<true, true>), grid, block, 0, stream, a, splits);
   else if (a.row_f32)
-    hipLaunchKernelGGL((combine_kernel<true, false>), grid, dim3(kCbThreads), 0, stream, a);
+    hipLaunchKernelGGL((combine_kernel<true, false>), grid, block, 0, stream, a, splits);
   else if (a.out_f32)
-    hipLaunchKernelGGL((combine_kernel<false, true>), grid, dim3(kCbThreads), 0, stream, a);
+    hipLaunchKernelGGL((combine_kernel<false, true>), grid, block, 0, stream, a, splits);
   else
-    hipLaunchKernelGGL((combine_kernel<false, false>), grid, dim3(kCbThreads), 0, stream, a);
+    hipLaunchKernelGGL((combine_kernel<false, false>), grid, block, 0, stream, a, splits);
   return hipGetLastError();
 }
 
 hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.tokens < kMaxGrid ? a.tokens : kMaxGrid));
+  const dim3 grid((unsigned)(a.tokens < kMaxGrid ? a.tokens : kMaxGrid)), block((unsigned)block_threads(a.n, kCbBwdThreads));
   if (a.dy_f32 && a.row_f32)
-    hipLaunchKernelGGL((combine_bwd_kernel<true, true>), grid, dim3(kCbThreads), 0, stream, a);
+    hipLaunchKernelGGL((combine_bwd_kernel<true, true>), grid, block, 0, stream, a);
   else if (a.dy_f32)
-    hipLaunchKernelGGL((combine_bwd_kernel<true, false>), grid, dim3(kCbThreads), 0, stream, a);
+    hipLaunchKernelGGL((combine_bwd_kernel<true, false>), grid, block, 0, stream, a);
   else if (a.row_f32)
-    hipLaunchKernelGGL((combine_bwd_kernel<false, true>), grid, dim3(kCbThreads), 0, stream, a);
+    hipLaunchKernelGGL((combine_bwd_kernel<false, true>), grid, block, 0, stream, a);
   else
-    hipLaunchKernelGGL((combine_bwd_kernel<false, false>), grid, dim3(kCbThreads), 0, stream, a);
+    hipLaunchKernelGGL((combine_bwd_kernel<false, false>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
