@@ -18,18 +18,10 @@ namespace fp8blk {
 namespace {
 
 constexpr float kFltMax = 3.402823466e38f;
-constexpr int kTokensPerWg = 4;
 
 __device__ __forceinline__ float load_logit(const void* l, bool f32, int64_t i) {
   if (f32) return reinterpret_cast<const float*>(l)[i];
   return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(l)[i] << 16);
-}
-
-template <typename T>
-__device__ __forceinline__ T wave_add(T v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-  return v;
 }
 
 // Orders a wave's own LDS reads and writes across its lanes (the hardware
@@ -255,19 +247,20 @@ __device__ __forceinline__ void select_exact(const RouteArgs& a, const float* l,
 // EPL consecutive logits of a token from expert e0 on; past the last expert,
 // whatever logits of the token (the caller masks them).
 template <int EPL>
-__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t row, int e0, bool vec, float* l) {
+__device__ __forceinline__ void load_logits(const void* logits, bool f32, int E, int64_t row, int e0, bool vec,
+                                            float* l) {
   static_assert(EPL % 4 == 0, "four at a time");
   if (vec) {
     // experts % 4 == 0 and rows aligned: four at a time are within the row or past it
 #pragma unroll
     for (int i = 0; i < EPL; i += 4) {
-      const int64_t at = row + (e0 + i < a.experts ? e0 + i : a.experts - 4);
-      if (a.logits_f32) {
-        const v4f v = *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(a.logits) + at);
+      const int64_t at = row + (e0 + i < E ? e0 + i : E - 4);
+      if (f32) {
+        const v4f v = *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(logits) + at);
 #pragma unroll
         for (int j = 0; j < 4; ++j) l[i + j] = v[j];
       } else {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(reinterpret_cast<const uint16_t*>(a.logits) + at);
+        const u32x2 w = *reinterpret_cast<const u32x2*>(reinterpret_cast<const uint16_t*>(logits) + at);
         l[i] = bf_lo(w.x);
         l[i + 1] = bf_hi(w.x);
         l[i + 2] = bf_lo(w.y);
@@ -277,7 +270,7 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t row, int
   } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      l[i] = load_logit(a.logits, a.logits_f32, row + (e0 + i < a.experts ? e0 + i : a.experts - 1));
+      l[i] = load_logit(logits, f32, row + (e0 + i < E ? e0 + i : E - 1));
   }
 }
 
@@ -315,7 +308,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int vec, int64_
   const int64_t t = tw + sub;
   const bool live = t < a.tokens;
   float l[EPL], bias[EPL], key[EPL], s[EPL];
-  load_logits<EPL>(a, (live ? t : a.tokens - 1) * E, e0, vec != 0, l);
+  load_logits<EPL>(a.logits, a.logits_f32, E, (live ? t : a.tokens - 1) * E, e0, vec != 0, l);
 #pragma unroll
   for (int i = 0; i < EPL; ++i) bias[i] = SCORED ? a.bias[e0 + i < E ? e0 + i : E - 1] : 0.f;
 #pragma unroll
@@ -443,88 +436,127 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int vec, int64_
     }
 }
 
-// One wave per token.  With v_j = scale * dw_j over the valid choices:
+// With v_j = scale * dw_j over the valid choices:
 //   sigmoid: dl = (v_j - [renorm] <v, s> / S) / [renorm] S * s (1 - s)
 //   softmax: dl = s (ds - <ds, s>), ds as above; with renorm <ds, s> = 0
 //            and the weights are a softmax over the choices alone
-__global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
+// G lanes per token (at least top_k: lane gl holds choice gl), EPL
+// consecutive experts per lane, as in route_kernel; chosen logits and their
+// gradients change lanes through LDS.  Bound by latency for a few thousand
+// tokens (4099 x 160 bf16: 4.8 us), then by its instructions: 16384 x 256
+// fp32 takes 13 us with softmax (2.6 TB/s) and 11 us renormalized.
+template <int G, int EPL>
+__global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a, int vec, int64_t t0) {
   extern __shared__ float smemf[];
+  constexpr int TPW = 64 / G;
   const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
-  const int E = a.experts;
-  float* acc = smemf + (size_t)wave * E;
+  const int gl = lane & (G - 1), sub = lane / G;
   const float none = -__builtin_inff();
-  for (int64_t t = (int64_t)blockIdx.x * kTokensPerWg + wave; t < a.tokens; t += (int64_t)gridDim.x * kTokensPerWg) {
-  float mx = none;
-  auto logit = [&](int e) -> float {
-    float l = load_logit(a.logits, a.logits_f32, t * E + e);
-    if (!(l > none)) l = none;
-    return l > kFltMax ? kFltMax : l;
-  };
-  for (int e = lane; e < E; e += 64) {
-    acc[e] = 0.f;
-    const float l = logit(e);
-    mx = mx > l ? mx : l;
-  }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, d, 64));
+  const int E = a.experts, e0 = gl * EPL;
+  float* mine = smemf + (size_t)(wave * TPW + sub) * (G * EPL);
+  const int64_t tw = t0 + ((int64_t)blockIdx.x * 4 + wave) * TPW;    // this wave's first token
+  if (tw >= a.tokens) return;
+  const bool live = tw + sub < a.tokens;
+  const int64_t t = live ? tw + sub : a.tokens - 1;
+  float l[EPL];
+  load_logits<EPL>(a.logits, a.logits_f32, E, t * E, e0, vec != 0, l);
   int id = -1;
-  float v = 0.f, cl = none;
-  if (lane < a.top_k) {
-    id = a.ids[t * a.top_k + lane];
-    if (id < 0 || id >= E) id = -1;
-    if (id >= 0) {
-      cl = logit(id);
-      if (!(cl > none)) id = -1;
-    }
-    if (id >= 0) v = a.scale * a.dweights[t * a.top_k + lane];
+  float v = 0.f;
+  if (gl < a.top_k) {
+    id = a.ids[t * a.top_k + gl];
+    v = a.scale * a.dweights[t * a.top_k + gl];
   }
-  float top = cl;
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d, 64));
-  float z = 1.f;
-  if (a.score == 0 && !a.renorm) {
+  for (int i = 0; i < EPL; ++i) {
+    l[i] = e0 + i < E ? clean(l[i]) : none;
+    mine[e0 + i] = l[i];
+  }
+  wave_fence();
+  float cl = none;
+  if (id >= 0 && id < E) cl = mine[id];
+  const bool ok = cl > none;        // neither left out nor masked
+  wave_fence();
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) mine[e0 + i] = 0.f;
+  float mx = 0.f, z = 1.f;
+  float s[EPL];
+  const bool whole = a.score == 0 && !a.renorm;     // the gradient reaches every expert
+  if (whole) {
+    mx = l[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) mx = __builtin_fmaxf(mx, l[i]);
+    mx = run_max<G>(mx, lane);
+    mx = mx > none ? mx : 0.f;
     z = 0.f;
-    for (int e = lane; e < E; e += 64) {
-      const float l = logit(e);
-      if (l > none) z += expf(l - mx);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      s[i] = expf(l[i] - mx);
+      z += s[i];
     }
-    z = wave_add(z);
+    z = run_add<G>(z, lane);
   }
   float dl = 0.f, back = 0.f;
   if (a.renorm) {
-    float s = 0.f;
-    const float base = a.score == 0 ? top : (top < 0.f ? top : 0.f);
-    if (id >= 0)
-      s = a.score == 0 ? expf(cl - base) : (cl >= 0.f ? 1.f / (1.f + expf(-cl)) : expf(cl - base) / (1.f + expf(cl)));
-    const float sum = wave_add(s);
-    const float p = id >= 0 ? s / sum : 0.f;       // the weight before scale
-    const float mean = wave_add(v * p);
-    dl = p * (v - mean);
-    if (a.score == 1 && id >= 0) dl *= 1.f / (1.f + expf(cl));
-  } else if (id >= 0) {
-    const float s = a.score == 0 ? expf(cl - mx) / z : 1.f / (1.f + expf(-cl));
-    dl = v * s;
+    const float top = run_max<G>(cl, lane);
+    const float base = a.score == 0 || top < 0.f ? top : 0.f;
+    const float c = ok ? choice_score(a.score, cl, base) : 0.f;
+    const float sum = run_add<G>(c, lane);
+    const float p = ok ? c / sum : 0.f;            // the weight before scale
+    const float mean = run_add<G>(ok ? v * p : 0.f, lane);
+    dl = ok ? p * (v - mean) : 0.f;
+    if (a.score == 1 && ok) dl *= 1.f / (1.f + expf(cl));
+  } else if (ok) {
+    const float c = a.score == 0 ? expf(cl - mx) / z : 1.f / (1.f + expf(-cl));
+    dl = v * c;
     if (a.score == 1) dl *= 1.f / (1.f + expf(cl));
   }
-  if (a.score == 0 && !a.renorm) back = wave_add(dl);
-  // choices in order, so that an expert listed twice adds up the same way
-  // every time
-  for (int j = 0; j < a.top_k; ++j) {
-    if (lane == j && id >= 0) acc[id] += dl;
-    __builtin_amdgcn_wave_barrier();
-    __threadfence_block();
+  if (whole) back = run_add<G>(dl, lane);
+  wave_fence();
+  // An expert listed twice adds up: its first lane takes the sum, in the
+  // order of the choices.
+  bool twice = false;
+  for (int j = 1; j < a.top_k; ++j) {
+    const int other = __shfl(id, sub * G + ((gl + j) & (G - 1)), 64);
+    twice = twice || (ok && other == id && ((gl + j) & (G - 1)) < a.top_k);
   }
-  for (int e = lane; e < E; e += 64) {
-    float d = acc[e];
-    if (a.score == 0 && !a.renorm) {
-      const float l = logit(e);
-      if (l > none) d -= back * (expf(l - mx) / z);
+  if (__builtin_amdgcn_ballot_w64(twice) == 0) {
+    if (ok) mine[id] = dl;
+  } else {
+#pragma clang loop unroll(disable)
+    for (int j = 0; j < a.top_k; ++j) {
+      if (gl == j && ok) mine[id] += dl;
+      wave_fence();
     }
-    if (a.logits_f32)
-      reinterpret_cast<float*>(a.dlogits)[t * E + e] = d;
-    else
-      reinterpret_cast<uint16_t*>(a.dlogits)[t * E + e] = (uint16_t)pack_bf16x2(d, 0.f);
   }
+  wave_fence();
+  if (!live) return;
+  float d[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    d[i] = mine[e0 + i];
+    if (whole && l[i] > none) d[i] -= back * (s[i] / z);
+  }
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < EPL; i += 4) {
+      if (e0 + i >= E) break;
+      if (a.logits_f32) {
+        *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.dlogits) + t * E + e0 + i) =
+            (v4f){d[i], d[i + 1], d[i + 2], d[i + 3]};
+      } else {
+        *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.dlogits) + t * E + e0 + i) =
+            (u32x2){pack_bf16x2(d[i], d[i + 1]), pack_bf16x2(d[i + 2], d[i + 3])};
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      if (e0 + i >= E) break;
+      if (a.logits_f32)
+        reinterpret_cast<float*>(a.dlogits)[t * E + e0 + i] = d[i];
+      else
+        reinterpret_cast<uint16_t*>(a.dlogits)[t * E + e0 + i] = (uint16_t)pack_bf16x2(d[i], 0.f);
+    }
   }
 }
 
@@ -749,11 +781,28 @@ hipError_t launch_route(const RouteArgs& args, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int G, int EPL>
+static void launch_route_bwd_as(const RouteBwdArgs& a, bool vec, hipStream_t stream) {
+  constexpr int kTokens = 4 * (64 / G);
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += kMaxGrid * kTokens) {
+    const int64_t wgs = (a.tokens - t0 + kTokens - 1) / kTokens;
+    hipLaunchKernelGGL((route_bwd_kernel<G, EPL>), dim3((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid)), dim3(256),
+                       (size_t)4 * 64 * EPL * 4, stream, a, vec ? 1 : 0, t0);
+  }
+}
+
 hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t stream) {
-  const int64_t wgs = (a.tokens + kTokensPerWg - 1) / kTokensPerWg;
-  const dim3 grid((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid));
-  hipLaunchKernelGGL(route_bwd_kernel, grid, dim3(64 * kTokensPerWg), (size_t)kTokensPerWg * a.experts * sizeof(float),
-                     stream, a);
+  const uintptr_t both = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits);
+  const bool vec = a.experts % 4 == 0 && (both & (a.logits_f32 ? 15 : 7)) == 0;
+  const int epl = a.experts > 512 ? 16 : a.experts > 256 ? 8 : 4;
+  int lanes = 8;                        // per token: one per choice at least
+  while (lanes < 64 && (lanes * epl < a.experts || lanes < a.top_k)) lanes *= 2;
+  if (epl == 16) launch_route_bwd_as<64, 16>(a, vec, stream);
+  else if (epl == 8) launch_route_bwd_as<64, 8>(a, vec, stream);
+  else if (lanes == 64) launch_route_bwd_as<64, 4>(a, vec, stream);
+  else if (lanes == 32) launch_route_bwd_as<32, 4>(a, vec, stream);
+  else if (lanes == 16) launch_route_bwd_as<16, 4>(a, vec, stream);
+  else launch_route_bwd_as<8, 4>(a, vec, stream);
   return hipGetLastError();
 }
 
