@@ -85,19 +85,20 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(CombineArgs a, int 
     }
     for (int j0 = 0; j0 < a.top_k; j0 += kBatch) {
       Chunk<ROW_F32> r[kBatch];
-      float w[kBatch];
+      int64_t s[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const int64_t s = j0 + j < a.top_k ? slot[j0 + j] : -1;
-        w[j] = s >= 0 && s < a.total_m ? wt[j0 + j] : 0.f;
-        r[j].load(row_buffer<ROW_F32>(a.rows, s, a.total_m, a.n), c);
+        s[j] = j0 + j < a.top_k ? slot[j0 + j] : -1;
+        r[j].load(row_buffer<ROW_F32>(a.rows, s[j], a.total_m, a.n), c);
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
+        if (s[j] < 0 || s[j] >= a.total_m) continue;      // uniform: not even +0 is added
+        const float w = wt[j0 + j];
         float f[8];
         r[j].get(f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w[j], f[i], acc[i]);
+        for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w, f[i], acc[i]);
       }
     }
     Chunk<OUT_F32> y;

@@ -76,6 +76,34 @@ def test_same_row_for_two_tokens():
     assert torch.equal(y, torch.stack([2 * rows[1].float(), rows[0].float() + rows[1].float()]))
 
 
+def test_left_out_pairs_add_nothing():
+    """Not even a zero: a residual of -0 stays -0."""
+    res = torch.full((2, 16), -0.0, dtype=BF, device="cuda")
+    slot = torch.tensor([[-1, -1, 4], [-1, 0, 9]], dtype=torch.int32, device="cuda")
+    rows = torch.full((4, 16), -0.0, dtype=BF, device="cuda")
+    y = fb.moe_combine(rows, slot, torch.ones((2, 3), device="cuda"), residual=res)
+    assert torch.all(torch.signbit(y))
+
+
+def test_rows_beyond_32_bit_offsets():
+    total, n = 300000, 16384
+    rows = torch.zeros((total, n), dtype=BF, device="cuda")
+    rows[-2:] = torch.randn((2, n), device="cuda").to(BF)
+    slot = torch.tensor([[total - 1, 0], [5, total - 2]], dtype=torch.int32, device="cuda")
+    w = torch.full((2, 2), 0.5, device="cuda")
+    y = fb.moe_combine(rows, slot, w, out_dtype=F32)
+    assert torch.equal(y, 0.5 * rows[-2:].flip(0).float())
+    dy = torch.randn((2, n), device="cuda").to(BF)
+    drows = torch.zeros_like(rows)
+    dw = torch.empty_like(w)
+    fb.fp8_moe_combine_backward(dy, rows, slot, w, drows, dw)
+    assert torch.equal(drows[-1], (0.5 * dy[0].float()).to(BF)) and torch.equal(drows[5], (0.5 * dy[1].float()).to(BF))
+    want = (dy.double() * rows[-2:].flip(0).double()).sum(1)
+    mag = (dy.double() * rows[-2:].flip(0).double()).abs().sum(1)
+    assert torch.all((torch.stack([dw[0, 0], dw[1, 1]]).double() - want).abs() <= n * 2.0 ** -24 * mag)
+    assert dw[0, 1] == 0 and dw[1, 0] == 0
+
+
 @pytest.mark.parametrize("tokens,top_k,n,total", SHAPES)
 @pytest.mark.parametrize("row_dtype", [BF, F32])
 @pytest.mark.parametrize("dy_dtype", [BF, F32])
