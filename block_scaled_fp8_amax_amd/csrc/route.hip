@@ -156,12 +156,14 @@ __device__ __forceinline__ void sort_falling(float* key, int* idx) {
 
 // What a run of G lanes knows of its token: its groups ranked.  LDS lkey
 // holds the token's ranking values (T), from which lane gl takes every
-// width-th of group gl / width.  Returns the group's score in its lanes.
+// width-th of group gl / width.  Leaves the group's two best values in k1
+// and k2 of its lanes and returns its score.
 template <int G, typename T>
-__device__ __forceinline__ T group_scores(const RouteArgs& a, const T* lkey, bool top2, int gl, int lane) {
+__device__ __forceinline__ T group_scores(const RouteArgs& a, const T* lkey, bool top2, int gl, int lane, T& k1,
+                                          T& k2) {
   const T none = -(T)__builtin_inff();
   const int width = 1 << a.log_width, grp = gl >> a.log_width;
-  T k1 = none, k2 = none;
+  k1 = k2 = none;
   if (grp < a.groups)
 #pragma clang loop unroll(disable)
     for (int i = gl - (grp << a.log_width); i < a.per; i += width) {
@@ -218,7 +220,8 @@ __device__ __forceinline__ void select_exact(const RouteArgs& a, const float* l,
   }
   wave_fence();
   if constexpr (GROUPS) {
-    const double score = group_scores<G>(a, lkey, top2, gl, lane);
+    double k1, k2;
+    const double score = group_scores<G>(a, lkey, top2, gl, lane, k1, k2);
     const int grp = gl >> a.log_width;
     int better = 0;
 #pragma clang loop unroll(disable)
@@ -354,8 +357,12 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int vec, int64_
     for (int i = 0; i < EPL; ++i) lkey[e0 + i] = SCORED || !top2 ? key[i] : (l[i] > none ? s[i] : none);
     wave_fence();
     const int grp = gl >> a.log_width;
-    const float score = group_scores<G>(a, lkey, top2, gl, lane);
-    const float gerr = (SCORED || top2) ? 4.f * (serr + 0x1p-23f * __builtin_fabsf(score)) : -1.f;
+    float k1, k2;
+    const float score = group_scores<G>(a, lkey, top2, gl, lane, k1, k2);
+    // twice a group's error: two keys' and three half steps of the larger
+    // (each pair of groups is looked at from both sides)
+    const float size = __builtin_fmaxf(__builtin_fabsf(k1), k2 > none ? __builtin_fabsf(k2) : 0.f);
+    const float gerr = (SCORED || top2) ? 4.f * (serr + 0x1p-23f * size) : -1.f;
     int better = 0;
 #pragma clang loop unroll(disable)
     for (int j = 0; j < a.groups; ++j) {

@@ -142,6 +142,43 @@ def test_h_written_over_the_residual():
            inplace=True)
 
 
+def test_h_written_over_x():
+    rng = np.random.default_rng(18)
+    xb, rb = _values(rng, 17, 1152, "normal"), _values(rng, 17, 1152, "normal")
+    x, r = bf16_from_bits(xb), bf16_from_bits(rb)
+    w = torch.ones(1152, device="cuda")
+    want = fb.rmsnorm_quantize(x, w, EPS, residual=r)
+    q, s = torch.empty_like(want["q"]), torch.empty_like(want["scale"])
+    fb.fp8_rmsnorm_quantize(x, w, EPS, "1x128", "ceil", q, s, residual=r, h=x)
+    assert torch.equal(x, want["h"]) and torch.equal(q.view(torch.uint8), want["q"].view(torch.uint8))
+    assert torch.equal(s, want["scale"])
+
+
+def test_rows_beyond_32_bit_offsets():
+    rows, cols = 262144 + 3, 16384
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn((3, cols), device="cuda").to(torch.bfloat16)
+    w = torch.ones(cols, device="cuda")
+    whole = fb.rmsnorm_quantize(x, w, EPS, save_rstd=True)
+    tail = fb.rmsnorm_quantize(x[-3:].contiguous(), w, EPS, save_rstd=True)
+    assert torch.equal(whole["q"][-3:].view(torch.uint8), tail["q"].view(torch.uint8))
+    assert torch.equal(whole["scale"][-3:], tail["scale"]) and torch.equal(whole["rstd"][-3:], tail["rstd"])
+    dx, dw = fb.rmsnorm_backward(x, x, w, whole["rstd"])
+    dx2, dw2 = fb.rmsnorm_backward(x[-3:].contiguous(), x[-3:].contiguous(), w, tail["rstd"])
+    assert torch.equal(dx[-3:], dx2)
+    assert torch.all((dw - dw2).abs() <= 2.0 ** -22 * dw2.abs())          # three rows, added in another order
+
+
+def test_same_bytes_every_time():
+    rng = np.random.default_rng(19)
+    h, dy = (bf16_from_bits(_values(rng, 3000, 1152, "normal")) for _ in range(2))
+    w, r = torch.ones(1152, device="cuda"), torch.rand(3000, device="cuda")
+    first = fb.rmsnorm_backward(dy, h, w, r)
+    for _ in range(5):
+        again = fb.rmsnorm_backward(dy, h, w, r)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1].view(torch.int32), again[1].view(torch.int32))
+
+
 def test_more_rows_than_workgroups():
     """Rows past the launch's largest grid are taken by the same workgroups."""
     rows, cols = (1 << 20) + 3, 128

@@ -120,6 +120,19 @@ def test_keys_closer_than_fp32_tells_apart(score, gs):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_sums_that_cancel(score):
+    """Two best keys of a group that are large and of opposite sign: their sum is small, its rounding is not."""
+    rng = np.random.default_rng(31)
+    l, l64 = _logits(rng, 300, 32, torch.float32)
+    bias = np.full(32, -5000.0)
+    for g in range(8):
+        bias[4 * g], bias[4 * g + 1] = 1000.0 + 0.001 * g, -1000.0 - 0.001 * g
+    bias = bias.astype(np.float32).astype(np.float64)
+    _check(l, l64, bias, 4, score, 8, 3, "top2")
+    _check(l, l64, bias, 4, score, 8, 1, "top2", renorm=True)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_masks(score, renorm):
     """Masked experts are never chosen; rows that mask everything, all but one, or whole groups; NaN and infinities."""
@@ -209,6 +222,32 @@ def test_backward_of_left_out_repeated_and_masked(score, renorm):
     dw = rng.standard_normal((6, 4)).astype(np.float32)
     got = _backward_check(l, l64, ids, dw, score, renorm, 1.0)
     assert np.all(got[2] == 0) and np.all(got[5] == 0) and got[4, 3] == 0
+
+
+def test_more_tokens_than_one_launch_takes():
+    """Tokens past the largest grid of a launch; 32 tokens of 8 experts to a workgroup."""
+    tokens = 32 * (1 << 20) + 37
+    l = torch.zeros((tokens, 8), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator("cuda").manual_seed(3)
+    l[-300:] = torch.randn((300, 8), device="cuda", generator=g).to(torch.bfloat16)
+    ids, w = fb.moe_route(l, 2, renorm=True)
+    i2, w2 = fb.moe_route(l[-300:].contiguous(), 2, renorm=True)
+    assert torch.equal(ids[-300:], i2) and torch.equal(w[-300:], w2)
+    assert torch.all(ids[:-300] == torch.tensor([0, 1], device="cuda", dtype=torch.int32))
+    dw = torch.ones_like(w)
+    dw[-300:] = torch.randn((300, 2), device="cuda", generator=g)
+    d = fb.moe_route_backward(l, ids, dw, renorm=True)
+    d2 = fb.moe_route_backward(l[-300:].contiguous(), i2, dw[-300:].contiguous(), renorm=True)
+    assert torch.equal(d[-300:], d2) and torch.all(d[:-300] == 0)
+
+
+def test_logits_beyond_32_bit_offsets():
+    tokens, experts = (1 << 21) + 11, 1024
+    l = torch.zeros((tokens, experts), dtype=torch.bfloat16, device="cuda")
+    l[-5:] = torch.randn((5, experts), device="cuda").to(torch.bfloat16)
+    ids, w = fb.moe_route(l, 8, score="sigmoid", bias=torch.zeros(experts, device="cuda"))
+    i2, w2 = fb.moe_route(l[-5:].contiguous(), 8, score="sigmoid", bias=torch.zeros(experts, device="cuda"))
+    assert torch.equal(ids[-5:], i2) and torch.equal(w[-5:], w2)
 
 
 def _plan_check(ids, experts):
