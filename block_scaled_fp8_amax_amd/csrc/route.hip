@@ -368,7 +368,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int vec, int64_
     for (int j = 0; j < a.groups; ++j) {
       const float o = __shfl(score, sub * G + (j << a.log_width), 64);
       better += o > score || (o == score && j < grp);
-      close = close || (j != grp && grp < a.groups && score > none && __builtin_fabsf(o - score) <= gerr);
+      // sums that leave the fp32 range differ by NaN and are close
+      close = close || (j != grp && grp < a.groups && k1 > none && !(__builtin_fabsf(o - score) > gerr));
     }
     drop_groups<EPL>(a, __builtin_amdgcn_ballot_w64(grp < a.groups && better < a.topk_groups), e0, sub * G, key);
   }

@@ -133,6 +133,20 @@ def test_group_sums_that_cancel(score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_group_sums_beyond_fp32(score, sign):
+    """Two keys of a group near the largest float: fp32 sums of +-inf would tie, or look like a group of none."""
+    rng = np.random.default_rng(32)
+    l, l64 = _logits(rng, 50, 32, torch.float32)
+    l[:, :4] = -float("inf")                                  # a group of none before the others
+    l64[:, :4] = -np.inf
+    size = np.repeat(np.array([0, 2, 3, 1, 2.5, 3.4, 3.3, 1.5]), 4) * 1e38
+    bias = (sign * size).astype(np.float32).astype(np.float64)
+    _check(l, l64, bias, 4, score, 8, 2, "top2")
+    _check(l, l64, bias, 4, score, 8, 7, "top2")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_masks(score, renorm):
     """Masked experts are never chosen; rows that mask everything, all but one, or whole groups; NaN and infinities."""
