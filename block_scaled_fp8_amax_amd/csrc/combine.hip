@@ -11,8 +11,9 @@ namespace {
 
 constexpr int kBatch = 8;            // choices whose rows are loaded together
 // Threads of a workgroup at most.  Forward, one chunk each: 16384 tokens of
-// eight rows of 7168 take 470 us (5.0 TB/s) with 128, 474 with 64, 493 with
-// 192 and 500 to 520 with 256 to 896.  Backward, a whole token: 4093 such
+// eight rows of 7168 take 462 us (5.1 TB/s) with 128; an earlier form of the
+// kernel 470 with 128, 474 with 64, 493 with 192 and 500 to 520 with 256 to
+// 896.  Backward, a whole token: 4093 such
 // tokens take 206 us (4.8 TB/s) with 512, 207 with 256, 212 with 128.
 constexpr int kCbThreads = 128;
 constexpr int kCbBwdThreads = 512;
@@ -190,7 +191,8 @@ hipError_t launch_combine(const CombineArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.tokens < kMaxGrid ? a.tokens : kMaxGrid)), block((unsigned)block_threads(a.n, kCbBwdThreads));
+  const dim3 grid((unsigned)(a.tokens < kMaxGrid ? a.tokens : kMaxGrid));
+  const dim3 block((unsigned)block_threads(a.n, kCbBwdThreads));
   if (a.dy_f32 && a.row_f32)
     hipLaunchKernelGGL((combine_bwd_kernel<true, true>), grid, block, 0, stream, a);
   else if (a.dy_f32)

@@ -10,7 +10,10 @@
 //
 // One workgroup per row.  Thread t holds the 8-element chunks t, t + T, ...
 // of the row in registers between the sum of squares and the encode, so the
-// row is read once; a 1x128 tile is 16 adjacent lanes, a 1x32 block 4.
+// row is read once; a 1x128 tile is 16 adjacent lanes, a 1x32 block 4.  Bound
+// by HBM for many rows: 16384 x 7168 with residual, h and y, 9 bytes per
+// element, in 186 us (5.7 TB/s; nontemporal accesses 183 us, but 9.4 against
+// 8.7 us for a thousand rows).  A few rows are bound by latency: 4.1 us.
 #include "device.h"
 #include "launch.h"
 
@@ -218,8 +221,8 @@ struct NormBwdParams {
 
 // Workgroup b takes the rows b, b + G, ...; the weight gradient of its rows
 // stays in registers and goes to the workspace once.  Bound by reading dy, h
-// and dres and writing dx: 8192 x 7168 in 88 us (5.3 TB/s) and 4 us for
-// the partials.  Two rows at a time, rows kept packed across the barrier and
+// and dres and writing dx: 8192 x 7168 in 88 us (5.3 TB/s) and 4 us for the
+// partials (two launches replayed: 96 us).  Two rows at a time, rows kept packed across the barrier and
 // dres loaded before it all took registers that cost a workgroup per CU, and
 // 10 to 60% more time.
 template <bool WF32, int CH>

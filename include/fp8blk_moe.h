@@ -52,7 +52,8 @@ typedef enum { FP8_GROUP_MAX = 0, FP8_GROUP_TOP2 = 1 } fp8_group_score;
  * and y is quantized per row in 1x128 tiles (scale = RN32(amax / 448),
  * code = e4m3(y / scale)) or 1x32 blocks (E8M0 exponent X by `rule`, code =
  * e4m3(y * 2^-X)) as fp8_block_quantize does, but from the fp32 y.  A tile
- * whose fp32 scale is 0 gets codes +-0.
+ * whose fp32 scale is 0 gets codes +-0.  Rows whose h or y leaves its range
+ * (bf16, fp32) have no defined codes.
  *
  * x        [rows x cols] bf16 (16-byte aligned);
  * residual optional (NULL = none) [rows x cols] bf16 (16-byte aligned);
@@ -173,8 +174,12 @@ int fp8_moe_plan_workspace(int64_t tokens, int top_k, int experts, size_t* bytes
  * fp8_nvfp4_matvec -- products of a few bf16 rows with an NVFP4 matrix:
  *   y[i][j] = sum over k of x[i][k] * e2m1(code[j][k]) * e4m3(S[j][k / 16]) * g[j / rows_per_tensor]
  * with exact products, fp32 sums (the scale g multiplies the sum) and one
- * rounding to y's type.  Meant for 1 to about 32 rows; more are taken 16 at
- * a time and read the weights again for each.
+ * rounding to y's type.  Meant for 1 to about 32 rows (of each group, in the
+ * grouped call); more are taken 16 or 32 at a time and read the weights
+ * again for each.  The order of a row's sum depends on the sizes of the call
+ * and of its group, so a row can differ in its last bits from the same row
+ * in a call of another size.  A scale byte that is NaN makes its products
+ * NaN.
  *
  * x [m x k] bf16 (16-byte aligned); q [n x k/2] codes, block_scale
  * [n x k/16], global_scale [n / rows_per_tensor] float as written by
@@ -229,8 +234,8 @@ int fp8_moe_combine(const void* rows, int row_type, int64_t total_m, const int32
  *   drows[slot[t][j]] = weights[t][j] * dy[t],  dweights[t][j] = <dy[t], rows[slot[t][j]]>
  * (the residual's gradient is dy itself).  drows is of row_type, rounded
  * once; rows that no slot names are left as they were.  Slots are distinct,
- * as fp8_moe_plan's are; a row that two slots name gets one of the two
- * gradients.  A slot outside [0, total_m) gets dweight 0.
+ * as fp8_moe_plan's are; a row that two slots name ends with elements of
+ * either gradient.  A slot outside [0, total_m) gets dweight 0.
  *
  * dy [tokens x n] bf16 or float per dy_type; other arguments as above.
  */

@@ -153,7 +153,8 @@ def _backward(m, x, res, dy):
     """Backward calls of one layer around the experts (whose own gradient is left to the caller): combination, weights
     to logits, logits and norm."""
     n, logits, ids, w, (off, row, slot) = _route(m, x, res)
-    d = (torch.arange(x.shape[0] * K, device="cuda")[:, None] % 7 + torch.arange(H, device="cuda") % 5).to(torch.bfloat16)
+    d = torch.arange(x.shape[0] * K, device="cuda")[:, None] % 7 + torch.arange(H, device="cuda") % 5
+    d = d.to(torch.bfloat16)
     drows, dw = fb.moe_combine_backward(dy, d, slot, w)
     dl = fb.moe_route_backward(logits, ids, dw, score="sigmoid", renorm=True, scale=2.5)
     dyn = (dl[:, :, None] * m["gate"].float()[None]).sum(1).to(torch.bfloat16)

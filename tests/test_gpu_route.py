@@ -278,7 +278,8 @@ def _plan_check(ids, experts):
 
 @pytest.mark.parametrize("tokens,top_k,experts", [(0, 2, 4), (1, 1, 1), (1, 8, 256), (5, 3, 7), (256, 8, 64),
                                                   (257, 8, 256), (1000, 6, 160), (4099, 8, 256), (700, 64, 1024),
-                                                  (131072, 1, 3), (2048, 1, 5), (2049, 1, 5), (300000, 1, 130), (35000, 8, 257)])
+                                                  (131072, 1, 3), (2048, 1, 5), (2049, 1, 5), (300000, 1, 130),
+                                                  (35000, 8, 257)])
 @pytest.mark.parametrize("kind", ["spread", "one expert", "left out"])
 def test_plan(tokens, top_k, experts, kind):
     print(f"[plan] {tokens} tokens, top {top_k} of {experts}, {kind}", flush=True)

@@ -110,7 +110,8 @@ def test_plan_validation(lib):
     assert need(8, 8, 64, ctypes.byref(size)) == OK and size.value == 0
     assert need(1 << 14, 8, 256, ctypes.byref(size)) == OK and 0 < size.value <= 1 << 20
     big = size.value
-    assert need(1 << 24, 64, 1024, ctypes.byref(size)) == OK and size.value == ((1 << 19) + 1) * 1024 * 4     # a count per expert and 2048 pairs
+    # a count per expert and 2048 pairs
+    assert need(1 << 24, 64, 1024, ctypes.byref(size)) == OK and size.value == ((1 << 19) + 1) * 1024 * 4
     assert need((1 << 24) + 1, 64, 1024, ctypes.byref(size)) == SHAPE
     call = _caller(lib.fp8_moe_plan, "ids tokens k experts ws bytes off row slot".split(),
                    [P, 1 << 14, 8, 256, P, big, P, P, P])
