@@ -104,7 +104,9 @@ struct RouteArgs {
   float scale;
   int32_t* ids;
   float* weights;
-  int per = 0, log_width = 0;   // experts per group, log2 of lanes per group (set by the launcher)
+  // set by the launcher: experts per group, log2 of the lanes that rank a group through LDS, and of those whose
+  // experts make up a group (-1 where lanes span groups)
+  int per = 0, log_width = 0, log_heads = -1;
   float inv_per = 0.f;
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);

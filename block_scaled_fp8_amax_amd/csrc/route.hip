@@ -36,33 +36,71 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
 }
 
-// The partner's value at step STEP of a butterfly over 2^6 lanes: after the
-// steps 0 .. n-1 of an associative operation each run of 2^n lanes holds its
-// result (the mirror steps pair lanes whose runs are complete already).
+// The two values of step STEP of a butterfly over 2^6 lanes, in either order:
+// after the steps 0 .. n-1 of a commutative operation each run of 2^n lanes
+// holds its result (the mirror steps pair lanes whose runs are complete
+// already; the swap steps leave the lower run's value in one register and
+// the upper run's in the other, for the lanes of both).
 template <int STEP>
-__device__ __forceinline__ uint32_t partner(uint32_t v, int lane) {
-  if constexpr (STEP == 0) return dpp<kQuadSwap1>(v);
-  if constexpr (STEP == 1) return dpp<kQuadSwap2>(v);
-  if constexpr (STEP == 2) return dpp<kRowHalfMirror>(v);
-  if constexpr (STEP == 3) return dpp<kRowMirror>(v);
+__device__ __forceinline__ void both(uint32_t v, uint32_t& a, uint32_t& b) {
+  a = v;
+  if constexpr (STEP == 0) b = dpp<kQuadSwap1>(v);
+  if constexpr (STEP == 1) b = dpp<kQuadSwap2>(v);
+  if constexpr (STEP == 2) b = dpp<kRowHalfMirror>(v);
+  if constexpr (STEP == 3) b = dpp<kRowMirror>(v);
   if constexpr (STEP == 4) {
-    const u32x2 r = __builtin_bit_cast(
-        u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
-    return (lane & 16) ? r.x : r.y;
+    const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+    a = r.x;
+    b = r.y;
   }
-  const u32x2 r = __builtin_bit_cast(
-      u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));
-  return (lane & 32) ? r.x : r.y;
+  if constexpr (STEP == 5) {
+    const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+    a = r.x;
+    b = r.y;
+  }
 }
 template <int STEP>
-__device__ __forceinline__ float partner(float v, int lane) {
-  return __uint_as_float(partner<STEP>(__float_as_uint(v), lane));
+__device__ __forceinline__ void both(int v, int& a, int& b) {
+  uint32_t x, y;
+  both<STEP>((uint32_t)v, x, y);
+  a = (int)x;
+  b = (int)y;
 }
 template <int STEP>
-__device__ __forceinline__ double partner(double v, int lane) {
+__device__ __forceinline__ void both(float v, float& a, float& b) {
+  uint32_t x, y;
+  both<STEP>(__float_as_uint(v), x, y);
+  a = __uint_as_float(x);
+  b = __uint_as_float(y);
+}
+template <int STEP>
+__device__ __forceinline__ void both(double v, double& a, double& b) {
   const u32x2 w = __builtin_bit_cast(u32x2, v);
-  return __builtin_bit_cast(double, (u32x2){partner<STEP>(w.x, lane), partner<STEP>(w.y, lane)});
+  u32x2 x, y;
+  uint32_t p, q;
+  both<STEP>(w.x, p, q);
+  x.x = p;
+  y.x = q;
+  both<STEP>(w.y, p, q);
+  x.y = p;
+  y.y = q;
+  a = __builtin_bit_cast(double, x);
+  b = __builtin_bit_cast(double, y);
 }
+
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return __builtin_fminf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ double smaller(double a, double b) { return a < b ? a : b; }
+__device__ __forceinline__ int larger(int a, int b) { return a > b ? a : b; }
+__device__ __forceinline__ int smaller(int a, int b) { return a < b ? a : b; }
+
+// A float as an int of the same order, and back.
+__device__ __forceinline__ int ordered(float f) {
+  const int i = (int)__float_as_uint(f);
+  return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float unordered(int i) { return __uint_as_float((uint32_t)(i ^ ((i >> 31) & 0x7FFFFFFF))); }
 
 // A logit or bias as the ranking takes it: NaN masks, +inf is the largest
 // float.
@@ -75,30 +113,38 @@ __device__ __forceinline__ float clean(float v) {
 // 1 / (2 per) at e + 1/2, far above the product's rounding.
 __device__ __forceinline__ int group_of(const RouteArgs& a, int e) { return (int)(((float)e + 0.5f) * a.inv_per); }
 
-template <int G, int STEP = 0>
-__device__ __forceinline__ float run_max(float v, int lane) {
-  if constexpr ((1 << STEP) < G)
-    return run_max<G, STEP + 1>(__builtin_fmaxf(v, partner<STEP>(v, lane)), lane);
-  else
+template <int G, typename T, int STEP = 0>
+__device__ __forceinline__ T run_max(T v) {
+  if constexpr ((1 << STEP) < G) {
+    T a, b;
+    both<STEP>(v, a, b);
+    return run_max<G, T, STEP + 1>(larger(a, b));
+  } else {
     return v;
+  }
 }
 template <int G, typename T, int STEP = 0>
-__device__ __forceinline__ T run_add(T v, int lane) {
-  if constexpr ((1 << STEP) < G)
-    return run_add<G, T, STEP + 1>(v + partner<STEP>(v, lane), lane);
-  else
+__device__ __forceinline__ T run_add(T v) {
+  if constexpr ((1 << STEP) < G) {
+    T a, b;
+    both<STEP>(v, a, b);
+    return run_add<G, T, STEP + 1>(a + b);
+  } else {
     return v;
+  }
 }
 // Best (key, index) of a run: highest key, lowest index among equals.
 template <int G, int STEP = 0>
-__device__ __forceinline__ void run_best(double& k, int& i, int lane) {
+__device__ __forceinline__ void run_best(double& k, int& i) {
   if constexpr ((1 << STEP) < G) {
-    const double ok = partner<STEP>(k, lane);
-    const int oi = (int)partner<STEP>((uint32_t)i, lane);
-    const bool take = ok > k || (ok == k && oi < i);
-    k = take ? ok : k;
-    i = take ? oi : i;
-    run_best<G, STEP + 1>(k, i, lane);
+    double ka, kb;
+    int ia, ib;
+    both<STEP>(k, ka, kb);
+    both<STEP>(i, ia, ib);
+    const bool take = kb > ka || (kb == ka && ib < ia);
+    k = take ? kb : ka;
+    i = take ? ib : ia;
+    run_best<G, STEP + 1>(k, i);
   }
 }
 
@@ -111,45 +157,63 @@ __device__ __forceinline__ float choice_score(int score, float l, float base) {
   return (l >= 0.f ? 1.f : base < 0.f ? __expf(l - base) : e) * __builtin_amdgcn_rcpf(1.f + e);
 }
 
-__device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
-__device__ __forceinline__ float smaller(float a, float b) { return __builtin_fminf(a, b); }
-__device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
-__device__ __forceinline__ double smaller(double a, double b) { return a < b ? a : b; }
-
 // The two largest values of runs of `width` (a power of two) lanes.
 template <int STEP, typename T>
-__device__ __forceinline__ void top2_step(T& k1, T& k2, int lane) {
-  const T o1 = partner<STEP>(k1, lane), o2 = partner<STEP>(k2, lane);
-  const T hi = larger(k1, o1), lo = smaller(k1, o1);
-  k2 = larger(lo, larger(k2, o2));
-  k1 = hi;
+__device__ __forceinline__ void top2_step(T& k1, T& k2) {
+  T a1, b1, a2, b2;
+  both<STEP>(k1, a1, b1);
+  both<STEP>(k2, a2, b2);
+  k2 = larger(smaller(a1, b1), larger(a2, b2));
+  k1 = larger(a1, b1);
 }
 template <typename T>
-__device__ __forceinline__ void run_top2(T& k1, T& k2, int width, int lane) {
-  if (width > 1) top2_step<0>(k1, k2, lane);
-  if (width > 2) top2_step<1>(k1, k2, lane);
-  if (width > 4) top2_step<2>(k1, k2, lane);
-  if (width > 8) top2_step<3>(k1, k2, lane);
-  if (width > 16) top2_step<4>(k1, k2, lane);
-  if (width > 32) top2_step<5>(k1, k2, lane);
+__device__ __forceinline__ void run_top2(T& k1, T& k2, int width) {
+  if (width > 1) top2_step<0>(k1, k2);
+  if (width > 2) top2_step<1>(k1, k2);
+  if (width > 4) top2_step<2>(k1, k2);
+  if (width > 8) top2_step<3>(k1, k2);
+  if (width > 16) top2_step<4>(k1, k2);
+  if (width > 32) top2_step<5>(k1, k2);
 }
 
 // Sorts a lane's EPL (key, index) pairs by falling key, equal keys in order
 // (odd-even transposition: only neighbours change places).
-template <int EPL, int R = 0, int I = 0>
-__device__ __forceinline__ void sort_falling(float* key, int* idx) {
+template <int EPL, typename T, int R = 0, int I = 0>
+__device__ __forceinline__ void sort_pairs(T* key, int* idx) {
   if constexpr (R < EPL) {
     if constexpr (I + 1 < EPL) {
       const bool sw = key[I + 1] > key[I];
-      const float ka = sw ? key[I + 1] : key[I], kb = sw ? key[I] : key[I + 1];
+      const T ka = larger(key[I], key[I + 1]), kb = smaller(key[I], key[I + 1]);
       const int ia = sw ? idx[I + 1] : idx[I], ib = sw ? idx[I] : idx[I + 1];
       key[I] = ka;
       key[I + 1] = kb;
       idx[I] = ia;
       idx[I + 1] = ib;
-      sort_falling<EPL, R, I + 2>(key, idx);
+      sort_pairs<EPL, T, R, I + 2>(key, idx);
     } else {
-      sort_falling<EPL, R + 1, (R + 1) & 1>(key, idx);
+      sort_pairs<EPL, T, R + 1, (R + 1) & 1>(key, idx);
+    }
+  }
+}
+
+// Sorts a lane's EPL keys by falling value: Batcher's odd-even merges (19
+// exchanges of 8 keys), unrolled in the types so that keys stay in registers.
+template <int EPL, int P = 1, int K = 1, int J = 0, int I = 0>
+__device__ __forceinline__ void sort_keys(int* key) {
+  if constexpr (P < EPL) {
+    if constexpr (K < 1) {
+      sort_keys<EPL, 2 * P, 2 * P, 0, 0>(key);
+    } else if constexpr (J + K >= EPL) {
+      sort_keys<EPL, P, K / 2, (K / 2) % P, 0>(key);
+    } else if constexpr (I >= K || I + J + K >= EPL) {
+      sort_keys<EPL, P, K, J + 2 * K, 0>(key);
+    } else {
+      if constexpr ((I + J) / (2 * P) == (I + J + K) / (2 * P)) {
+        const int a = larger(key[I + J], key[I + J + K]), b = smaller(key[I + J], key[I + J + K]);
+        key[I + J] = a;
+        key[I + J + K] = b;
+      }
+      sort_keys<EPL, P, K, J, I + 1>(key);
     }
   }
 }
@@ -159,8 +223,7 @@ __device__ __forceinline__ void sort_falling(float* key, int* idx) {
 // width-th of group gl / width.  Leaves the group's two best values in k1
 // and k2 of its lanes and returns its score.
 template <int G, typename T>
-__device__ __forceinline__ T group_scores(const RouteArgs& a, const T* lkey, bool top2, int gl, int lane, T& k1,
-                                          T& k2) {
+__device__ __forceinline__ T group_scores(const RouteArgs& a, const T* lkey, bool top2, int gl, T& k1, T& k2) {
   const T none = -(T)__builtin_inff();
   const int width = 1 << a.log_width, grp = gl >> a.log_width;
   k1 = k2 = none;
@@ -171,7 +234,7 @@ __device__ __forceinline__ T group_scores(const RouteArgs& a, const T* lkey, boo
       k2 = larger(k2, smaller(k1, k));
       k1 = larger(k1, k);
     }
-  run_top2(k1, k2, width, lane);
+  run_top2(k1, k2, width);
   return top2 && k2 > none ? k1 + k2 : k1;
 }
 
@@ -189,11 +252,38 @@ __device__ __forceinline__ void drop_groups(const RouteArgs& a, unsigned long lo
   }
 }
 
+// The top_k experts of a run whose lanes hold their keys as sort_pairs leaves
+// them, above nokey where there is an expert: into sel, -1 where there is
+// none.  Equal keys go by lane, and so by expert.
+template <int G, int EPL, typename T>
+__device__ __forceinline__ void choose(T* key, const int* idx, T nokey, int top_k, int e0, int gl, int sub, int* sel) {
+  uint64_t order = 0;                 // the lane's experts in the order of its keys, 4 bits each
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) order |= (uint64_t)(uint32_t)idx[i] << (4 * i);
+#pragma clang loop unroll(disable)
+  for (int r = gl; r < top_k; r += G) sel[r] = -1;
+  wave_fence();
+#pragma clang loop unroll(disable)
+  for (int r = 0; r < top_k; ++r) {
+    const T w = run_max<G>(key[0]);
+    const bool best = w > nokey && key[0] == w;
+    const unsigned long long eq = __builtin_amdgcn_ballot_w64(best);
+    const unsigned long long run = G == 64 ? eq : (eq >> (sub * G)) & ((1ull << (G & 63)) - 1);
+    if (best && __builtin_ctzll(run) == gl) {
+      sel[r] = e0 + (int)(order & 15);
+      order >>= 4;
+#pragma unroll
+      for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
+      key[EPL - 1] = nokey;
+    }
+  }
+}
+
 // The wave's tokens again with keys in double precision: sel as the fp32
 // pass below leaves it.
 template <int G, int EPL, bool SCORED, bool GROUPS>
 __device__ __forceinline__ void select_exact(const RouteArgs& a, const float* l, const float* bias, float mx, int gl,
-                                             int sub, int lane, double* lkey, int* sel) {
+                                             int sub, double* lkey, int* sel) {
   const double none = -__builtin_inf();
   const int e0 = gl * EPL;
   const bool top2 = GROUPS && a.group_score == 1;
@@ -204,60 +294,65 @@ __device__ __forceinline__ void select_exact(const RouteArgs& a, const float* l,
       key[i] = l[i] > -__builtin_inff() ? exp((double)l[i] - (double)mx) : 0.0;
       z += key[i];
     }
-    z = run_add<G>(z, lane);
+    z = run_add<G>(z);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = key[i] / z;
   } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = 1.0 / (1.0 + exp(-(double)l[i]));
   }
+  const bool heads = SCORED && GROUPS && a.log_heads >= 0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const bool in = l[i] > -__builtin_inff();
     const double rank = in ? (SCORED ? key[i] + (double)bias[i] : top2 ? key[i] : (double)l[i]) : none;
-    if constexpr (GROUPS) lkey[e0 + i] = rank;
+    if (GROUPS && !heads) lkey[e0 + i] = rank;
     key[i] = SCORED ? rank : (double)l[i];
   }
-  wave_fence();
+  int idx[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) idx[i] = i;
+  if (heads) sort_pairs<EPL>(key, idx);
   if constexpr (GROUPS) {
-    double k1, k2;
-    const double score = group_scores<G>(a, lkey, top2, gl, lane, k1, k2);
-    const int grp = gl >> a.log_width;
+    wave_fence();
+    const int log_width = heads ? a.log_heads : a.log_width, grp = gl >> log_width;
+    double k1, k2, score;
+    if (heads) {
+      k1 = key[0];
+      k2 = key[1];
+      run_top2(k1, k2, 1 << log_width);
+      score = top2 && k2 > none ? k1 + k2 : k1;
+    } else {
+      score = group_scores<G>(a, lkey, top2, gl, k1, k2);
+    }
     int better = 0;
 #pragma clang loop unroll(disable)
     for (int j = 0; j < a.groups; ++j) {
-      const double o = __shfl(score, sub * G + (j << a.log_width), 64);
+      const double o = __shfl(score, sub * G + (j << log_width), 64);
       better += o > score || (o == score && j < grp);
     }
-    drop_groups<EPL>(a, __builtin_amdgcn_ballot_w64(grp < a.groups && better < a.topk_groups), e0, sub * G, key);
+    const bool stays = grp < a.groups && better < a.topk_groups;
+    if (heads)
+      key[0] = stays ? key[0] : none;
+    else
+      drop_groups<EPL>(a, __builtin_amdgcn_ballot_w64(stays), e0, sub * G, key);
   }
-#pragma clang loop unroll(disable)
-  for (int r = 0; r < a.top_k; ++r) {
-    double bk = none;
-    int bi = e0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      bi = key[i] > bk ? e0 + i : bi;
-      bk = larger(bk, key[i]);
-    }
-    run_best<G>(bk, bi, lane);
-    if (gl == 0) sel[r] = bk > none ? bi : -1;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = bi == e0 + i ? none : key[i];
-  }
+  if (!heads) sort_pairs<EPL>(key, idx);
+  choose<G, EPL>(key, idx, none, a.top_k, e0, gl, sub, sel);
 }
 
-// EPL consecutive logits of a token from expert e0 on; past the last expert,
-// whatever logits of the token (the caller masks them).
+// EPL consecutive values of a row from expert e0 on, -inf past the last
+// expert.  vec: experts % 4 == 0 and aligned for four values at a time, which
+// are then all within the row or all past it.
 template <int EPL>
 __device__ __forceinline__ void load_logits(const void* logits, bool f32, int E, int64_t row, int e0, bool vec,
                                             float* l) {
   static_assert(EPL % 4 == 0, "four at a time");
   if (vec) {
-    // experts % 4 == 0 and rows aligned: four at a time are within the row or past it
 #pragma unroll
     for (int i = 0; i < EPL; i += 4) {
-      const int64_t at = row + (e0 + i < E ? e0 + i : E - 4);
+      const bool in = e0 + i < E;
+      const int64_t at = row + (in ? e0 + i : E - 4);
       if (f32) {
         const v4f v = *reinterpret_cast<const v4f*>(reinterpret_cast<const float*>(logits) + at);
 #pragma unroll
@@ -269,27 +364,36 @@ __device__ __forceinline__ void load_logits(const void* logits, bool f32, int E,
         l[i + 2] = bf_lo(w.y);
         l[i + 3] = bf_hi(w.y);
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) l[i + j] = in ? l[i + j] : -__builtin_inff();
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
+    for (int i = 0; i < EPL; ++i) {
       l[i] = load_logit(logits, f32, row + (e0 + i < E ? e0 + i : E - 1));
+      l[i] = e0 + i < E ? l[i] : -__builtin_inff();
+    }
   }
 }
 
 // Bound by the vector instructions and the latency of top_k dependent
 // rounds, not by reading the logits: 16384 tokens of 256 experts, top 8, take
-// 13 us (1.3 TB/s) plain and 26 us with a bias and groups.
+// 11 us (1.5 TB/s) plain and 18 us with a bias and groups.
 //
 // G lanes per token (64 / G tokens per wave), EPL consecutive experts per
-// lane.  Keys in fp32, sorted within each lane; a round takes the largest
-// head of a run of G lanes (a butterfly of G lanes and a ballot: the lowest
-// lane with it holds the lowest expert) and moves that lane's list on.
+// lane.  Keys are ints of the order of the fp32 ranking values, sorted within
+// each lane; a round takes the largest head of a run of G lanes (a butterfly)
+// and moves that lane's list on.
 //
-// Where keys are scores, the fp32 ones are off by at most serr (below) and
-// half a step, so a choice between keys further apart than twice that is the
-// one double precision makes; a wave with a closer one chooses again in
-// double precision (some tens of 16384 tokens of 256 experts).
+// Where keys are scores, the low bits of a key hold its expert's place in the
+// lane, which makes an exchange of the sort two instructions (with the place
+// beside the key, five) and leaves kKeyErr of the key's precision; the fp32
+// score is off by at most serr (below).  A choice between keys further apart
+// than twice both is the one double precision makes; a wave with a closer one
+// chooses again in double precision (about a hundred of 16384 tokens of 256
+// experts, whose tail is 4 of the 18 us).  Groups that whole lanes make up
+// are ranked from the heads of the sorted lists (16384 tokens, 8 groups of
+// 32: 18.7 us, through LDS 22.4), others through LDS.
 template <int G, int EPL, bool SCORED, bool GROUPS>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int vec, int64_t t0) {
   extern __shared__ double smem[];
@@ -305,23 +409,24 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int vec, int64_
   int* sel = reinterpret_cast<int*>(mine + kKeyBytes) + sub * 64;
   const bool top2 = GROUPS && a.group_score == 1;
   const int e0 = gl * EPL;
+  // a ranking value's distance from its key, relative
+  constexpr float kKeyErr = SCORED ? EPL * 0x1p-23f : 0.f;
 
   const int64_t tw = t0 + ((int64_t)blockIdx.x * 4 + wave) * TPW;    // this wave's first token
   if (tw >= a.tokens) return;
   const int64_t t = tw + sub;
   const bool live = t < a.tokens;
-  float l[EPL], bias[EPL], key[EPL], s[EPL];
-  load_logits<EPL>(a.logits, a.logits_f32, E, (live ? t : a.tokens - 1) * E, e0, vec != 0, l);
+  float l[EPL], bias[EPL], rank[EPL], s[EPL];
+  load_logits<EPL>(a.logits, a.logits_f32, E, (live ? t : a.tokens - 1) * E, e0, (vec & 1) != 0, l);
+  if constexpr (SCORED) load_logits<EPL>(a.bias, true, E, 0, e0, (vec & 2) != 0, bias);
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) bias[i] = SCORED ? a.bias[e0 + i < E ? e0 + i : E - 1] : 0.f;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) l[i] = e0 + i < E ? clean(l[i]) : none;
+  for (int i = 0; i < EPL; ++i) l[i] = clean(l[i]);
   float mx = l[0];
 #pragma unroll
   for (int i = 1; i < EPL; ++i) mx = __builtin_fmaxf(mx, l[i]);
   float z = 1.f, pmax = 1.f;
   if (a.score == 0) {
-    mx = run_max<G>(mx, lane);
+    mx = run_max<G>(mx);
     z = 0.f;
     const float m = mx > none ? mx : 0.f;
 #pragma unroll
@@ -329,7 +434,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int vec, int64_
       s[i] = __expf(l[i] - m);
       z += s[i];
     }
-    z = run_add<G>(z, lane);
+    z = run_add<G>(z);
     const float r = 1.f / z;
     pmax = r;
 #pragma unroll
@@ -347,69 +452,99 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int vec, int64_
   bool close = false;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    bias[i] = clean(bias[i]);
-    key[i] = SCORED ? (l[i] > none ? s[i] + bias[i] : none) : l[i];
+    if constexpr (SCORED) bias[i] = clean(bias[i]);
+    rank[i] = SCORED ? (l[i] > none ? s[i] + bias[i] : none) : l[i] + 0.f;      // -0 is 0
   }
-  if constexpr (GROUPS) {
-    // keys to LDS, then `width` lanes per group
-    wave_fence();
+  int key[EPL], idx[EPL];
+  const int nokey = ordered(none);       // keys up to this one are no keys
+  const bool heads = SCORED && GROUPS && a.log_heads >= 0;
+  auto make_keys = [&]() {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) lkey[e0 + i] = SCORED || !top2 ? key[i] : (l[i] > none ? s[i] : none);
-    wave_fence();
-    const int grp = gl >> a.log_width;
-    float k1, k2;
-    const float score = group_scores<G>(a, lkey, top2, gl, lane, k1, k2);
-    // twice a group's error: two keys' and three half steps of the larger
-    // (each pair of groups is looked at from both sides)
+    for (int i = 0; i < EPL; ++i) {
+      key[i] = SCORED ? (ordered(rank[i]) & -EPL) | i : ordered(rank[i]);
+      idx[i] = i;
+    }
+    if constexpr (SCORED)
+      sort_keys<EPL>(key);
+    else
+      sort_pairs<EPL>(key, idx);
+  };
+  if constexpr (GROUPS) {
+    const int log_width = heads ? a.log_heads : a.log_width, grp = gl >> log_width;
+    float score, k1, k2;
+    if (heads) {
+      make_keys();
+      int i1 = key[0], i2 = key[1];
+      run_top2(i1, i2, 1 << log_width);
+      k1 = i1 > nokey ? unordered(i1) : none;
+      k2 = i2 > nokey ? unordered(i2) : none;
+      score = top2 && k2 > none ? k1 + k2 : k1;
+    } else {
+      // keys to LDS, then `width` lanes per group
+      wave_fence();
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) lkey[e0 + i] = SCORED || !top2 ? rank[i] : (l[i] > none ? s[i] : none);
+      wave_fence();
+      score = group_scores<G>(a, lkey, top2, gl, k1, k2);
+    }
+    // twice a group's error: two keys' and half a step of their sum, at most
+    // a step of the larger (each pair of groups is looked at from both sides)
     const float size = __builtin_fmaxf(__builtin_fabsf(k1), k2 > none ? __builtin_fabsf(k2) : 0.f);
-    const float gerr = (SCORED || top2) ? 4.f * (serr + 0x1p-23f * size) : -1.f;
-    int better = 0;
+    const float gerr = (SCORED || top2) ? 4.f * (serr + (kKeyErr + 0x1p-23f) * size) : -1.f;
+    int better = 0, near = 0;
 #pragma clang loop unroll(disable)
     for (int j = 0; j < a.groups; ++j) {
-      const float o = __shfl(score, sub * G + (j << a.log_width), 64);
+      const float o = __shfl(score, sub * G + (j << log_width), 64);
       better += o > score || (o == score && j < grp);
       // sums that leave the fp32 range differ by NaN and are close
-      close = close || (j != grp && grp < a.groups && k1 > none && !(__builtin_fabsf(o - score) > gerr));
+      near += !(__builtin_fabsf(o - score) > gerr);
     }
-    drop_groups<EPL>(a, __builtin_amdgcn_ballot_w64(grp < a.groups && better < a.topk_groups), e0, sub * G, key);
-  }
-  int idx[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) idx[i] = e0 + i;
-  sort_falling<EPL>(key, idx);
-#pragma clang loop unroll(disable)
-  for (int r = gl; r < 64; r += G) sel[r] = -1;
-  wave_fence();
-  float last = __builtin_inff(), gap = __builtin_inff(), big = 0.f;   // big: largest key looked at, by magnitude
-  auto look = [&](float w) {
-    gap = __builtin_fminf(gap, last - w);
-    big = __builtin_fmaxf(big, w > none ? __builtin_fabsf(w) : 0.f);
-    last = w;
-  };
-#pragma clang loop unroll(disable)
-  for (int r = 0; r < a.top_k; ++r) {
-    const float w = run_max<G>(key[0], lane);
-    look(w);
-    const unsigned long long eq = __builtin_amdgcn_ballot_w64(key[0] == w && w > none);
-    const unsigned long long run = G == 64 ? eq : (eq >> (sub * G)) & ((1ull << (G & 63)) - 1);
-    if (run != 0 && __builtin_ctzll(run) == gl) {
-      sel[r] = idx[0];
-#pragma unroll
-      for (int i = 0; i + 1 < EPL; ++i) {
-        key[i] = key[i + 1];
-        idx[i] = idx[i + 1];
-      }
-      key[EPL - 1] = none;
+    close = near > 1 && grp < a.groups && k1 > none;        // one of them is the group itself
+    const bool stays = grp < a.groups && better < a.topk_groups;
+    if (heads) {
+      key[0] = stays ? key[0] : nokey;
+    } else {
+      drop_groups<EPL>(a, __builtin_amdgcn_ballot_w64(stays), e0, sub * G, rank);
+      make_keys();
     }
+  } else {
+    make_keys();
   }
   if constexpr (SCORED) {
-    look(run_max<G>(key[0], lane));   // the first one left out
-    close = close || gap <= 2.f * serr + 0x1p-22f * big;
+    float last = __builtin_inff(), gap = __builtin_inff();
+    auto look = [&](int w) {
+      const float f = unordered(w);       // NaN where there is no key, which fminf passes over
+      gap = __builtin_fminf(gap, __builtin_fmaf(-2.f * kKeyErr - 0x1p-22f, __builtin_fabsf(f), last - f));
+      last = f;
+    };
+    bool tie = false;
+#pragma clang loop unroll(disable)
+    for (int r = gl; r < a.top_k; r += G) sel[r] = -1;
+    wave_fence();
+#pragma clang loop unroll(disable)
+    for (int r = 0; r < a.top_k; ++r) {
+      const int w = run_max<G>(key[0]);
+      look(w);
+      const bool any = w > nokey, first = any && key[0] == w;
+      // runs with a key have one lane with it, or a tie
+      tie = tie || __builtin_popcountll(__builtin_amdgcn_ballot_w64(first)) * G !=
+                       __builtin_popcountll(__builtin_amdgcn_ballot_w64(any));
+      if (first) {
+        sel[r] = e0 + (key[0] & (EPL - 1));
+#pragma unroll
+        for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
+        key[EPL - 1] = nokey;
+      }
+    }
+    look(run_max<G>(key[0]));   // the first one left out
+    close = close || tie || gap <= 2.f * serr;
+  } else {
+    choose<G, EPL>(key, idx, nokey, a.top_k, e0, gl, sub, sel);
   }
   wave_fence();
   if constexpr (SCORED || GROUPS) {
     if (__builtin_amdgcn_ballot_w64(close && live) != 0) {
-      select_exact<G, EPL, SCORED, GROUPS>(a, l, bias, mx, gl, sub, lane,
+      select_exact<G, EPL, SCORED, GROUPS>(a, l, bias, mx, gl, sub,
                                            reinterpret_cast<double*>(mine) + sub * (G * EPL), sel);
       wave_fence();
     }
@@ -427,12 +562,12 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int vec, int64_
     float top = c0;
 #pragma clang loop unroll(disable)
     for (int r = gl + G; r < a.top_k; r += G) top = __builtin_fmaxf(top, chosen_logit(r));
-    top = run_max<G>(top, lane);
+    top = run_max<G>(top);
     base = a.score == 0 || top < 0.f ? top : 0.f;
     float sum = choice(c0, base);
 #pragma clang loop unroll(disable)
     for (int r = gl + G; r < a.top_k; r += G) sum += choice(chosen_logit(r), base);
-    sum = run_add<G>(sum, lane);
+    sum = run_add<G>(sum);
     norm = a.scale / sum;
   }
   if (live)
@@ -476,7 +611,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a, int vec,
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    l[i] = e0 + i < E ? clean(l[i]) : none;
+    l[i] = clean(l[i]);
     mine[e0 + i] = l[i];
   }
   wave_fence();
@@ -493,7 +628,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a, int vec,
     mx = l[0];
 #pragma unroll
     for (int i = 1; i < EPL; ++i) mx = __builtin_fmaxf(mx, l[i]);
-    mx = run_max<G>(mx, lane);
+    mx = run_max<G>(mx);
     mx = mx > none ? mx : 0.f;
     z = 0.f;
 #pragma unroll
@@ -501,16 +636,16 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a, int vec,
       s[i] = expf(l[i] - mx);
       z += s[i];
     }
-    z = run_add<G>(z, lane);
+    z = run_add<G>(z);
   }
   float dl = 0.f, back = 0.f;
   if (a.renorm) {
-    const float top = run_max<G>(cl, lane);
+    const float top = run_max<G>(cl);
     const float base = a.score == 0 || top < 0.f ? top : 0.f;
     const float c = ok ? choice_score(a.score, cl, base) : 0.f;
-    const float sum = run_add<G>(c, lane);
+    const float sum = run_add<G>(c);
     const float p = ok ? c / sum : 0.f;            // the weight before scale
-    const float mean = run_add<G>(ok ? v * p : 0.f, lane);
+    const float mean = run_add<G>(ok ? v * p : 0.f);
     dl = ok ? p * (v - mean) : 0.f;
     if (a.score == 1 && ok) dl *= 1.f / (1.f + expf(cl));
   } else if (ok) {
@@ -518,7 +653,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a, int vec,
     dl = v * c;
     if (a.score == 1) dl *= 1.f / (1.f + expf(cl));
   }
-  if (whole) back = run_add<G>(dl, lane);
+  if (whole) back = run_add<G>(dl);
   wave_fence();
   // An expert listed twice adds up: its first lane takes the sum, in the
   // order of the choices.
@@ -749,16 +884,16 @@ int64_t plan_workspace_bytes(int64_t pairs, int experts) {
 }
 
 template <int G, int EPL, bool SCORED, bool GROUPS>
-static void launch_route_as(const RouteArgs& a, bool vec, hipStream_t stream) {
+static void launch_route_as(const RouteArgs& a, int vec, hipStream_t stream) {
   constexpr int kTokens = 4 * (64 / G);
   for (int64_t t0 = 0; t0 < a.tokens; t0 += kMaxGrid * kTokens) {
     const int64_t wgs = (a.tokens - t0 + kTokens - 1) / kTokens;
     hipLaunchKernelGGL((route_kernel<G, EPL, SCORED, GROUPS>), dim3((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid)),
-                       dim3(256), (size_t)4 * (64 * EPL * 8 + (64 / G) * 256), stream, a, vec ? 1 : 0, t0);
+                       dim3(256), (size_t)4 * (64 * EPL * 8 + (64 / G) * 256), stream, a, vec, t0);
   }
 }
 template <int G, int EPL>
-static void launch_route_as(const RouteArgs& a, bool vec, hipStream_t stream) {
+static void launch_route_as(const RouteArgs& a, int vec, hipStream_t stream) {
   if (a.bias && a.groups > 1) launch_route_as<G, EPL, true, true>(a, vec, stream);
   else if (a.bias) launch_route_as<G, EPL, true, false>(a, vec, stream);
   else if (a.groups > 1) launch_route_as<G, EPL, false, true>(a, vec, stream);
@@ -767,11 +902,14 @@ static void launch_route_as(const RouteArgs& a, bool vec, hipStream_t stream) {
 
 hipError_t launch_route(const RouteArgs& args, hipStream_t stream) {
   RouteArgs a = args;
-  const bool vec = a.experts % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & (a.logits_f32 ? 15 : 7)) == 0;
+  const bool fours = a.experts % 4 == 0;
+  const int vec = (fours && (reinterpret_cast<uintptr_t>(a.logits) & (a.logits_f32 ? 15 : 7)) == 0 ? 1 : 0) |
+                  (fours && (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0 ? 2 : 0);
   // Experts per lane: four up to 256 experts; eight for many tokens, where
-  // the butterflies over fewer lanes count (16384 tokens of 256 experts: 12.7
-  // us against 14.8, of 128: 7.3 against 8.6) and the longer lists' latency
-  // does not (one token: 4.1 us against 3.6).
+  // the butterflies over fewer lanes count (16384 tokens of 256 experts: 11.0
+  // us against 12.7, of 128: 6.3 against 7.3; sixteen: 12.9 us) and the longer
+  // lists' latency does not (1024 tokens: 4.2 us against 3.8, 9.6 against 7.3
+  // with groups).
   const int epl = a.experts > 512 ? 16 : a.experts > 256 || (a.experts > 64 && a.tokens >= 4096) ? 8 : 4;
   int lanes = 8;                        // per token, and one per group at least
   while (lanes < 64 && (lanes * epl < a.experts || lanes < a.groups)) lanes *= 2;
@@ -779,6 +917,9 @@ hipError_t launch_route(const RouteArgs& args, hipStream_t stream) {
   a.inv_per = 1.0f / (float)a.per;
   a.log_width = 0;
   while ((2 << a.log_width) * a.groups <= lanes) ++a.log_width;
+  a.log_heads = -1;
+  for (int w = 0; epl << w <= a.per; ++w)
+    if (epl << w == a.per) a.log_heads = w;
   if (epl == 16) launch_route_as<64, 16>(a, vec, stream);
   else if (epl == 8 && lanes == 64) launch_route_as<64, 8>(a, vec, stream);
   else if (epl == 8 && lanes == 32) launch_route_as<32, 8>(a, vec, stream);
