@@ -318,7 +318,11 @@ __device__ __forceinline__ void mfma_rows(const MatvecArgs& a, int grp, int lo, 
       for (int i = 0; i < XI; ++i)
         *reinterpret_cast<u32x4*>(lds + S::kCodes + S::kScales + (2 * i + (lane >> 5)) * S::kXRow + (lane & 31) * 16) =
             cx[i];
-      load(s + KS);
+      // With 32 rows of x (16 loads a step) the step past the last one is not
+      // loaded: 8192 x 7168 in 15.2 us, 16.4 with it.  With fewer rows, or the
+      // loads of AL false, the branch cost more than those loads (4096 x 16384
+      // at 16 rows: 12.9 us, 12.2 without).
+      if (!(AL && MX == 32) || s + KS < steps) load(s + KS);
       __builtin_amdgcn_sched_barrier(0);
       wave_fence();
       u32x4 xf[CT][8];
@@ -413,7 +417,11 @@ void launch_tiles(const MatvecArgs& a, int64_t active, hipStream_t stream) {
 // 2048: 5.8 us, against 7.3 with 8 waves to a tile), and four on large grids
 // (64 groups of 16 rows, 7168 x 2048: 155 us, 171 with two).  With one or
 // two rows there is little x to share (8192 x 4096: 6.4 us with 4 waves to a
-// tile, 7.1 with two tiles).
+// tile, 7.1 with two tiles).  One tile per workgroup spends as much of the
+// address unit on x as on weights, so it loads no more rows than it needs
+// (4096 x 7168: 6.4 us for up to 4 rows, 6.7 for up to 8, 7.4 for up to 16),
+// except for groups, of which one may have many more rows than the others;
+// two steps in flight, or half a tile per workgroup, gained nothing.
 template <bool AL>
 void launch_rows(const MatvecArgs& a, int64_t active, int64_t tiles, int64_t rows, hipStream_t stream) {
   if (rows <= 2 && !a.offsets) {
@@ -422,7 +430,11 @@ void launch_rows(const MatvecArgs& a, int64_t active, int64_t tiles, int64_t row
     else
       launch_tiles<AL, 1, 2, 4>(a, active, stream);
   } else if (rows <= 16) {
-    if (tiles <= 256)
+    if (tiles <= 256 && rows <= 4 && !a.offsets)
+      launch_tiles<AL, 1, 4, 8>(a, active, stream);
+    else if (tiles <= 256 && rows <= 8 && !a.offsets)
+      launch_tiles<AL, 1, 8, 8>(a, active, stream);
+    else if (tiles <= 256)
       launch_tiles<AL, 1, 16, 8>(a, active, stream);
     else if (tiles <= 1024)
       launch_tiles<AL, 2, 16, 4>(a, active, stream);
