@@ -1,7 +1,10 @@
 // Weighted combination of the experts' rows (gfx950) and its gradients:
 //   y[t] = residual[t] + sum_j w[t][j] R[slot[t][j]]     (fp32, j ascending)
 //   dR[slot[t][j]] = w[t][j] dy[t],  dw[t][j] = <dy[t], R[slot[t][j]]>
-// Bound by reading (and writing) top_k rows per token.
+// Bound by reading (and writing) top_k rows per token.  The rows of KB
+// choices are loaded together, KB the power of two that top_k takes, eight at
+// most: a load of nothing costs the address unit as much as any (635 tokens
+// of one row of 7168, backward: 6.1 us, 14.2 with eight).
 #include "device.h"
 #include "launch.h"
 
@@ -9,7 +12,6 @@ namespace fp8blk {
 
 namespace {
 
-constexpr int kBatch = 8;            // choices whose rows are loaded together
 // Threads of a workgroup at most.  Forward, one chunk each: 16384 tokens of
 // eight rows of 7168 take 462 us (5.1 TB/s) with 128; an earlier form of the
 // kernel 470 with 128, 474 with 64, 493 with 192 and 500 to 520 with 256 to
@@ -68,7 +70,7 @@ struct Chunk {
 
 // A workgroup takes blockDim chunks of one token; `splits` workgroups make up
 // a token.
-template <bool ROW_F32, bool OUT_F32>
+template <bool ROW_F32, bool OUT_F32, int KB>
 __global__ __launch_bounds__(kCbThreads) void combine_kernel(CombineArgs a, int splits) {
   for (int64_t wg = blockIdx.x; wg < a.tokens * splits; wg += gridDim.x) {
     const int64_t t = wg / splits;
@@ -84,16 +86,16 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(CombineArgs a, int 
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     }
-    for (int j0 = 0; j0 < a.top_k; j0 += kBatch) {
-      Chunk<ROW_F32> r[kBatch];
-      int64_t s[kBatch];
+    for (int j0 = 0; j0 < a.top_k; j0 += KB) {
+      Chunk<ROW_F32> r[KB];
+      int64_t s[KB];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
+      for (int j = 0; j < KB; ++j) {
         s[j] = j0 + j < a.top_k ? slot[j0 + j] : -1;
         r[j].load(row_buffer<ROW_F32>(a.rows, s[j], a.total_m, a.n), c);
       }
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
+      for (int j = 0; j < KB; ++j) {
         if (s[j] < 0 || s[j] >= a.total_m) continue;      // uniform: not even +0 is added
         const float w = wt[j0 + j];
         float f[8];
@@ -108,19 +110,20 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(CombineArgs a, int 
   }
 }
 
-// One workgroup per token, kBatch choices at a time: dy is read once for all
+// One workgroup per token, KB choices at a time: dy is read once for all
 // of them, and their dot products are summed over the workgroup together.
-template <bool DY_F32, bool ROW_F32>
+template <bool DY_F32, bool ROW_F32, int KB>
 __global__ __launch_bounds__(kCbBwdThreads) void combine_bwd_kernel(CombineBwdArgs a) {
-  __shared__ float red[kCbBwdThreads / 64][kBatch];
+  __shared__ float red[2][kCbBwdThreads / 64][KB];     // of this batch and the one before
   const int nch = (int)(a.n / 8), t = (int)threadIdx.x, threads = (int)blockDim.x;
+  int turn = 0;
   for (int64_t tok = blockIdx.x; tok < a.tokens; tok += gridDim.x) {
     const Buffer dyb = row_buffer<DY_F32>(a.dy, tok, a.tokens, a.n);
-    for (int j0 = 0; j0 < a.top_k; j0 += kBatch) {
-      Buffer rb[kBatch], db[kBatch];
-      float w[kBatch], dot[kBatch];
+    for (int j0 = 0; j0 < a.top_k; j0 += KB, turn ^= 1) {
+      Buffer rb[KB], db[KB];
+      float w[KB], dot[KB];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
+      for (int j = 0; j < KB; ++j) {
         const int64_t s = j0 + j < a.top_k ? a.slot[tok * a.top_k + j0 + j] : -1;
         w[j] = s >= 0 && s < a.total_m ? a.weights[tok * a.top_k + j0 + j] : 0.f;
         rb[j] = row_buffer<ROW_F32>(a.rows, s, a.total_m, a.n);
@@ -129,14 +132,14 @@ __global__ __launch_bounds__(kCbBwdThreads) void combine_bwd_kernel(CombineBwdAr
       }
       for (int c = t; c < nch; c += threads) {
         Chunk<DY_F32> dy;
-        Chunk<ROW_F32> r[kBatch];
+        Chunk<ROW_F32> r[KB];
         dy.load(dyb, c);
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) r[j].load(rb[j], c);
+        for (int j = 0; j < KB; ++j) r[j].load(rb[j], c);
         float d[8];
         dy.get(d);
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
+        for (int j = 0; j < KB; ++j) {
           float f[8], g[8];
           r[j].get(f);
 #pragma unroll
@@ -150,57 +153,72 @@ __global__ __launch_bounds__(kCbBwdThreads) void combine_bwd_kernel(CombineBwdAr
         }
       }
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) dot[j] += __shfl_xor(dot[j], d, 64);
-        if ((t & 63) == 0) red[t >> 6][j] = dot[j];
+      for (int j = 0; j < KB; ++j) {
+        dot[j] = wave_add(dot[j]);
+        if ((t & 63) == 0) red[turn][t >> 6][j] = dot[j];
       }
       __syncthreads();
-      if (t < kBatch && j0 + t < a.top_k) {
+      if (t < KB && j0 + t < a.top_k) {
         float s = 0.f;
-        for (int v = 0; v < threads / 64; ++v) s += red[v][t];
+        for (int v = 0; v < threads / 64; ++v) s += red[turn][v][t];
         a.dweights[tok * a.top_k + j0 + t] = s;
       }
-      __syncthreads();
     }
   }
 }
 
-// Whole waves for a row of n, at most `most` threads.
+// Whole waves for a row of n: at most `most` threads, evenly loaded.
 int block_threads(int64_t n, int most) {
-  const int64_t need = (n / 8 + 63) / 64 * 64;
-  return (int)(need < 64 ? 64 : need < most ? need : most);
+  const int64_t chunks = n / 8, turns = (chunks + most - 1) / most;
+  const int64_t need = turns > 0 ? (chunks + turns - 1) / turns : 1;
+  return (int)((need + 63) / 64 * 64);
+}
+
+template <int KB>
+void launch_combine_of(const CombineArgs& a, hipStream_t stream) {
+  const int threads = a.n / 8 < kCbThreads ? block_threads(a.n, kCbThreads) : kCbThreads;
+  const int splits = (int)((a.n / 8 + threads - 1) / threads);
+  const int64_t wgs = a.tokens * splits;
+  const dim3 grid((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid)), block((unsigned)threads);
+  if (a.row_f32 && a.out_f32)
+    hipLaunchKernelGGL((combine_kernel<true, true, KB>), grid, block, 0, stream, a, splits);
+  else if (a.row_f32)
+    hipLaunchKernelGGL((combine_kernel<true, false, KB>), grid, block, 0, stream, a, splits);
+  else if (a.out_f32)
+    hipLaunchKernelGGL((combine_kernel<false, true, KB>), grid, block, 0, stream, a, splits);
+  else
+    hipLaunchKernelGGL((combine_kernel<false, false, KB>), grid, block, 0, stream, a, splits);
+}
+
+template <int KB>
+void launch_combine_bwd_of(const CombineBwdArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)(a.tokens < kMaxGrid ? a.tokens : kMaxGrid));
+  const dim3 block((unsigned)block_threads(a.n, kCbBwdThreads));
+  if (a.dy_f32 && a.row_f32)
+    hipLaunchKernelGGL((combine_bwd_kernel<true, true, KB>), grid, block, 0, stream, a);
+  else if (a.dy_f32)
+    hipLaunchKernelGGL((combine_bwd_kernel<true, false, KB>), grid, block, 0, stream, a);
+  else if (a.row_f32)
+    hipLaunchKernelGGL((combine_bwd_kernel<false, true, KB>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((combine_bwd_kernel<false, false, KB>), grid, block, 0, stream, a);
 }
 
 }  // namespace
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t stream) {
-  const int threads = block_threads(a.n, kCbThreads);
-  const int splits = (int)((a.n / 8 + threads - 1) / threads);
-  const int64_t wgs = a.tokens * splits;
-  const dim3 grid((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid)), block((unsigned)threads);
-  if (a.row_f32 && a.out_f32)
-    hipLaunchKernelGGL((combine_kernel<true, true>), grid, block, 0, stream, a, splits);
-  else if (a.row_f32)
-    hipLaunchKernelGGL((combine_kernel<true, false>), grid, block, 0, stream, a, splits);
-  else if (a.out_f32)
-    hipLaunchKernelGGL((combine_kernel<false, true>), grid, block, 0, stream, a, splits);
-  else
-    hipLaunchKernelGGL((combine_kernel<false, false>), grid, block, 0, stream, a, splits);
+  if (a.top_k == 1) launch_combine_of<1>(a, stream);
+  else if (a.top_k == 2) launch_combine_of<2>(a, stream);
+  else if (a.top_k <= 4) launch_combine_of<4>(a, stream);
+  else launch_combine_of<8>(a, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.tokens < kMaxGrid ? a.tokens : kMaxGrid));
-  const dim3 block((unsigned)block_threads(a.n, kCbBwdThreads));
-  if (a.dy_f32 && a.row_f32)
-    hipLaunchKernelGGL((combine_bwd_kernel<true, true>), grid, block, 0, stream, a);
-  else if (a.dy_f32)
-    hipLaunchKernelGGL((combine_bwd_kernel<true, false>), grid, block, 0, stream, a);
-  else if (a.row_f32)
-    hipLaunchKernelGGL((combine_bwd_kernel<false, true>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((combine_bwd_kernel<false, false>), grid, block, 0, stream, a);
+  if (a.top_k == 1) launch_combine_bwd_of<1>(a, stream);
+  else if (a.top_k == 2) launch_combine_bwd_of<2>(a, stream);
+  else if (a.top_k <= 4) launch_combine_bwd_of<4>(a, stream);
+  else launch_combine_bwd_of<8>(a, stream);
   return hipGetLastError();
 }
 

@@ -65,6 +65,26 @@ constexpr int kRowHalfMirror = 0x141; // lane i <-> 7-i within each 8 lanes
 constexpr int kRowMirror = 0x140;     // lane i <-> 15-i within each 16 lanes
 
 template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+
+// Sum over the 64 lanes of a wave, in every lane: runs of 2, 4, 8 and 16
+// lanes, then rows and halves of the wave (each pair of runs added to the
+// same value in both).
+__device__ __forceinline__ float wave_add(float v) {
+  v = dpp_add<kQuadSwap1>(v);
+  v = dpp_add<kQuadSwap2>(v);
+  v = dpp_add<kRowHalfMirror>(v);
+  v = dpp_add<kRowMirror>(v);
+  const uint32_t a = __float_as_uint(v);
+  const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a, a, false, false));
+  const uint32_t b = __float_as_uint(__uint_as_float(r.x) + __uint_as_float(r.y));
+  const u32x2 h = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(b, b, false, false));
+  return __uint_as_float(h.x) + __uint_as_float(h.y);
+}
+
+template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
   uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
   return v > o ? v : o;

@@ -99,11 +99,6 @@ struct Run {
   uint32_t s;
 };
 
-template <int CTRL>
-__device__ __forceinline__ float dpp_add(float v) {
-  return v + __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
-}
-
 template <bool OUT_F32>
 __device__ __forceinline__ void store_y(const MatvecArgs& a, int grp, int64_t row, int64_t j, float v) {
   v *= a.global_scale[((int64_t)grp * a.n + j) / a.rows_per_tensor];

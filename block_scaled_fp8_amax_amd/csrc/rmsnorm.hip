@@ -21,22 +21,16 @@ namespace fp8blk {
 
 namespace {
 
-__device__ __forceinline__ float group_add64(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
-  return v;
-}
-
 // Sum over the workgroup (its waves' sums added in wave order, so the
-// result does not depend on timing); red holds 16 floats.
+// result does not depend on timing); red holds 16 floats, which are free
+// again after the workgroup's next barrier.
 __device__ __forceinline__ float block_sum(float v, float* red) {
-  v = group_add64(v);
+  v = wave_add(v);
   const int waves = (int)(blockDim.x >> 6);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   float s = 0.f;
   for (int i = 0; i < waves; ++i) s += red[i];
-  __syncthreads();
   return s;
 }
 
@@ -99,9 +93,10 @@ __device__ __forceinline__ uint32_t e8m0_code_f32(uint32_t bits) {
 // BLK 32 or 128; CH chunks per thread.
 template <int BLK, bool FLOOR, bool WF32, int CH>
 __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormParams p) {
-  __shared__ float red[16];
+  __shared__ float red[2][2][16];         // of this row and the one before, the sum and the rescaled one
   const int T = (int)blockDim.x, t = (int)threadIdx.x;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
   const int64_t base = row * p.nch;
   float f[CH][8];
   float ss = 0.f;
@@ -125,7 +120,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormParams p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(f[i][j], f[i][j], ss);
   }
-  ss = block_sum(ss, red);
+  ss = block_sum(ss, red[turn][0]);
   float rstd = 1.0f / sqrtf(ss / p.cols + p.eps);
   if (!(ss < __builtin_inff())) {
     // squares left the fp32 range: the same with h 2^-64 (uniform branch)
@@ -137,7 +132,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormParams p) {
         const float d = f[i][j] * 0x1p-64f;
         s2 = __builtin_fmaf(d, d, s2);
       }
-    s2 = block_sum(s2, red);
+    s2 = block_sum(s2, red[turn][1]);
     rstd = 0x1p-64f / sqrtf(s2 / p.cols + p.eps * 0x1p-128f);
   }
   if (p.rstd && t == 0) p.rstd[row] = rstd;
@@ -227,14 +222,15 @@ struct NormBwdParams {
 // 10 to 60% more time.
 template <bool WF32, int CH>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
-  __shared__ float red[16];
+  __shared__ float red[2][16];            // of this row and the one before
   const int T = (int)blockDim.x, t = (int)threadIdx.x;
+  int turn = 0;
   float acc[CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
     const int64_t base = row * p.nch;
     const float rstd = p.rstd[row];
     float xh[CH][8], wd[CH][8];
@@ -260,7 +256,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
         dot = __builtin_fmaf(wd[i][j], xh[i][j], dot);
       }
     }
-    const float c1 = block_sum(dot, red) / p.cols;
+    const float c1 = block_sum(dot, red[turn]) / p.cols;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = t + i * T;
