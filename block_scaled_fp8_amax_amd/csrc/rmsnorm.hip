@@ -320,15 +320,20 @@ void row_shape(int nch, int64_t rows, int* ch, int* threads) {
   *threads = ((nch + *ch - 1) / *ch + 63) / 64 * 64;
 }
 
-// Workgroups of the backward pass: 16 waves per CU, and two workgroups where
-// one has more than eight, so that one's loads run beside the other's
-// barrier (8192 x 7168: 99 us against 118 with one; 4096 x 2048: 20 us with
-// four, 23 with eight).
+// Workgroups of the backward pass: 16 waves per CU, four workgroups at most,
+// and two where one has more than eight waves, so that one's loads run beside
+// the other's barrier (8192 x 7168: 84 us, 94 with one, 100 with four; 8192 x
+// 512: 13 us with four, 21 with sixteen).  A workgroup takes two rows and,
+// past 256 workgroups, four, so that the partial sums stay a small part of
+// the traffic (500 x 7168: 15 us, 21 with one row each; 2352 x 512: 9 us, 14
+// with one).
 int64_t bwd_parts(int64_t rows, int threads, int ch) {
   const int waves = threads / 64, least = ch == 1 ? 2 : 1;
-  const int per_cu = 16 / waves > least ? 16 / waves : least;
-  const int64_t wgs = 256 * (int64_t)per_cu;
-  return rows < wgs ? rows : wgs;
+  int per_cu = 16 / waves > least ? 16 / waves : least;
+  per_cu = per_cu < 4 ? per_cu : 4;
+  const int64_t most = 256 * (int64_t)per_cu;
+  const int64_t want = rows <= 64 ? rows : rows <= 128 ? 64 : rows <= 512 ? rows / 2 : rows <= 1024 ? 256 : rows / 4;
+  return want < most ? want : most;
 }
 
 }  // namespace

@@ -7,8 +7,8 @@ roundings, within D = 2^-17.  From there:
   * codes: rounding is monotone, so a code lies between the codes of the exact quotient times (1 - D) and (1 + D);
   * bf16 outputs add half a step, 2^-8;
   * gradients: dx adds a dot product over the row, off by at most 2^-18 of its terms' magnitudes; dw is a sum over
-    the rows in at most 2^8 dependent additions (one per 256 rows or more in a workgroup, then a tree over the
-    partials), so within 2^-16 of the magnitudes for the row counts here.
+    the rows in at most 2^8 dependent additions (four rows, or a 256th of them, in a workgroup, then a tree over
+    the partials), so within 2^-16 of the magnitudes for the row counts here.
 """
 
 import numpy as np
