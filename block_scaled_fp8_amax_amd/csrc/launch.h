@@ -136,6 +136,7 @@ struct MatvecArgs {
   int64_t groups, total_m, n, k;
   void* y;
   bool out_f32;
+  int64_t slice = 0;          // rows of x per workgroup without offsets (set by the launcher)
 };
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream);
 

@@ -374,8 +374,13 @@ template <bool AL, int R, int MX, int KS, bool OUT_F32>
 __global__ __launch_bounds__(64 * KS) void matvec_kernel(MatvecArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[KS * Stage<R, MX>::kBytes];
   const int t = (int)threadIdx.x;
-  int grp = 0, lo = 0, hi = (int)a.total_m;
-  if (a.offsets && !nth_group(a, (int)blockIdx.y, t & 63, &grp, &lo, &hi)) return;
+  int grp = 0, lo = 0, hi = 0;
+  if (a.offsets) {
+    if (!nth_group(a, (int)blockIdx.y, t & 63, &grp, &lo, &hi)) return;
+  } else {
+    lo = (int)(blockIdx.y * a.slice);
+    hi = lo + (int)a.slice < (int)a.total_m ? lo + (int)a.slice : (int)a.total_m;
+  }
   mfma_rows<AL, R, MX, KS, OUT_F32>(a, grp, lo, hi, (int64_t)blockIdx.x * (16 * R), smem, t,
                                     __builtin_amdgcn_readfirstlane(t >> 6));
 }
@@ -397,8 +402,8 @@ __global__ __launch_bounds__(64) void matvec_stream_kernel(MatvecArgs a) {
 }
 
 template <bool AL, int R, int MX, int KS>
-void launch_tiles(const MatvecArgs& a, int64_t active, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.n + 16 * R - 1) / (16 * R)), (unsigned)active);
+void launch_tiles(const MatvecArgs& a, int64_t slices, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.n + 16 * R - 1) / (16 * R)), (unsigned)slices);
   if (a.out_f32)
     hipLaunchKernelGGL((matvec_kernel<AL, R, MX, KS, true>), grid, dim3(64 * KS), 0, stream, a);
   else
@@ -418,42 +423,54 @@ void launch_tiles(const MatvecArgs& a, int64_t active, hipStream_t stream) {
 // except for groups, of which one may have many more rows than the others;
 // two steps in flight, or half a tile per workgroup, gained nothing.
 template <bool AL>
-void launch_rows(const MatvecArgs& a, int64_t active, int64_t tiles, int64_t rows, hipStream_t stream) {
+void launch_rows(const MatvecArgs& a, int64_t slices, int64_t tiles, int64_t rows, hipStream_t stream) {
   if (rows <= 2 && !a.offsets) {
     if (tiles <= 256)
-      launch_tiles<AL, 1, 2, 8>(a, active, stream);
+      launch_tiles<AL, 1, 2, 8>(a, slices, stream);
     else
-      launch_tiles<AL, 1, 2, 4>(a, active, stream);
+      launch_tiles<AL, 1, 2, 4>(a, slices, stream);
   } else if (rows <= 16) {
     if (tiles <= 256 && rows <= 4 && !a.offsets)
-      launch_tiles<AL, 1, 4, 8>(a, active, stream);
+      launch_tiles<AL, 1, 4, 8>(a, slices, stream);
     else if (tiles <= 256 && rows <= 8 && !a.offsets)
-      launch_tiles<AL, 1, 8, 8>(a, active, stream);
+      launch_tiles<AL, 1, 8, 8>(a, slices, stream);
     else if (tiles <= 256)
-      launch_tiles<AL, 1, 16, 8>(a, active, stream);
+      launch_tiles<AL, 1, 16, 8>(a, slices, stream);
     else if (tiles <= 1024)
-      launch_tiles<AL, 2, 16, 4>(a, active, stream);
+      launch_tiles<AL, 2, 16, 4>(a, slices, stream);
     else
-      launch_tiles<AL, 4, 16, 4>(a, active, stream);
+      launch_tiles<AL, 4, 16, 4>(a, slices, stream);
   } else {
     if (tiles <= 256)
-      launch_tiles<AL, 1, 32, 8>(a, active, stream);
+      launch_tiles<AL, 1, 32, 8>(a, slices, stream);
     else if (tiles <= 1024)
-      launch_tiles<AL, 2, 32, 4>(a, active, stream);
+      launch_tiles<AL, 2, 32, 4>(a, slices, stream);
     else
-      launch_tiles<AL, 4, 32, 2>(a, active, stream);
+      launch_tiles<AL, 4, 32, 2>(a, slices, stream);
   }
 }
 
 }  // namespace
 
-hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream) {
+hipError_t launch_matvec(const MatvecArgs& args, hipStream_t stream) {
+  MatvecArgs a = args;
   // non-empty groups at most, and rows per group at least, if they are even
   const int64_t active = a.offsets ? (a.groups < a.total_m ? a.groups : a.total_m) : 1;
-  const int64_t rows = (a.total_m + active - 1) / active;
+  int64_t rows = (a.total_m + active - 1) / active;
   const int64_t tiles = (a.n + 15) / 16 * active;
   const bool al = a.k % 64 == 0 && ((reinterpret_cast<uintptr_t>(a.q) & 15) == 0) &&
                   ((reinterpret_cast<uintptr_t>(a.block_scale) & 3) == 0);
+  // Where tiles leave CUs idle, more than eight rows are shared out among
+  // workgroups (1000 x 7184: 16 rows in 7.3 us, in one slice 8.0; 32 rows in
+  // 8.4 and 11.4; slices of four took 7.9 and 8.3, and 8 rows of 2000 x 7184
+  // 7.6 in two slices, 7.1 in one).
+  int64_t slices = active;
+  a.slice = a.total_m;
+  if (!a.offsets && tiles <= 128 && rows > 8) {
+    const int64_t most = 256 / tiles < (rows + 7) / 8 ? 256 / tiles : (rows + 7) / 8;
+    a.slice = rows = (a.total_m + most - 1) / most;
+    slices = (a.total_m + rows - 1) / rows;
+  }
   if (al && rows <= 2 && tiles > 1024) {
     const dim3 grid((unsigned)((a.n + 31) / 32), (unsigned)active);
     if (a.out_f32)
@@ -461,9 +478,9 @@ hipError_t launch_matvec(const MatvecArgs& a, hipStream_t stream) {
     else
       hipLaunchKernelGGL(matvec_stream_kernel<false>, grid, dim3(64), 0, stream, a);
   } else if (al) {
-    launch_rows<true>(a, active, tiles, rows, stream);
+    launch_rows<true>(a, slices, tiles, rows, stream);
   } else {
-    launch_rows<false>(a, active, tiles, rows, stream);
+    launch_rows<false>(a, slices, tiles, rows, stream);
   }
   return hipGetLastError();
 }

@@ -76,7 +76,8 @@ def test_random(m, n, k, dtype):
 @pytest.mark.parametrize("m,n,k", [(1, 4112, 320), (2, 5000, 192), (9, 5008, 192), (20, 5008, 208), (2, 16400, 64),
                                    (1, 16401, 576), (30, 16400, 128), (12, 16400, 80), (16, 16401, 64), (2, 16400, 48),
                                    (50, 300, 1024), (31, 4097, 272), (3, 300, 2064), (4, 130, 4096), (5, 520, 2320),
-                                   (8, 4096, 2048), (7, 33, 6160), (32, 4200, 1280), (17, 100, 4160), (29, 90, 2192)])
+                                   (8, 4096, 2048), (7, 33, 6160), (32, 4200, 1280), (17, 100, 4160), (29, 90, 2192),
+                                   (9, 16, 512), (100, 64, 1024), (33, 2048, 528), (1000, 40, 256), (17, 2033, 64)])
 def test_exact_on_larger_grids(m, n, k):
     """Row and tile counts on both sides of every choice of launch shape."""
     print(f"[matvec] larger grid {m}x{n}x{k}", flush=True)
