@@ -13,10 +13,10 @@ namespace fp8blk {
 namespace {
 
 // Threads of a workgroup at most.  Forward, one chunk each: 16384 tokens of
-// eight rows of 7168 take 462 us (5.1 TB/s) with 128; an earlier form of the
+// eight rows of 7168 take 412 us (5.7 TB/s) with 128; an earlier form of the
 // kernel 470 with 128, 474 with 64, 493 with 192 and 500 to 520 with 256 to
-// 896.  Backward, a whole token: 4093 such
-// tokens take 206 us (4.8 TB/s) with 512, 207 with 256, 212 with 128.
+// 896.  Backward, a whole token: 4093 such tokens take 203 us (4.9 TB/s) with
+// 512; the earlier form 206, 207 with 256, 212 with 128.
 constexpr int kCbThreads = 128;
 constexpr int kCbBwdThreads = 512;
 
@@ -34,16 +34,17 @@ __device__ __forceinline__ Buffer row_buffer(const void* rows, int64_t s, int64_
 
 // Eight consecutive elements, chunk c of a row; bytes past the row are zeros
 // and stores there are dropped.
-template <bool F32>
+template <bool F32, bool NT>
 struct Chunk {
+  static constexpr int kPolicy = NT ? 2 : 0;      // the nontemporal bit
   u32x4 v[F32 ? 2 : 1];
   __device__ __forceinline__ void load(Buffer b, int c) {
-    v[0] = __builtin_amdgcn_raw_buffer_load_b128(b, (uint32_t)c * (F32 ? 32 : 16), 0, 0);
-    if constexpr (F32) v[1] = __builtin_amdgcn_raw_buffer_load_b128(b, (uint32_t)c * 32 + 16, 0, 0);
+    v[0] = __builtin_amdgcn_raw_buffer_load_b128(b, (uint32_t)c * (F32 ? 32 : 16), 0, kPolicy);
+    if constexpr (F32) v[1] = __builtin_amdgcn_raw_buffer_load_b128(b, (uint32_t)c * 32 + 16, 0, kPolicy);
   }
   __device__ __forceinline__ void store(Buffer b, int c) const {
-    __builtin_amdgcn_raw_buffer_store_b128(v[0], b, (uint32_t)c * (F32 ? 32 : 16), 0, 0);
-    if constexpr (F32) __builtin_amdgcn_raw_buffer_store_b128(v[1], b, (uint32_t)c * 32 + 16, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(v[0], b, (uint32_t)c * (F32 ? 32 : 16), 0, kPolicy);
+    if constexpr (F32) __builtin_amdgcn_raw_buffer_store_b128(v[1], b, (uint32_t)c * 32 + 16, 0, kPolicy);
   }
   __device__ __forceinline__ void get(float* f) const {
     if constexpr (F32) {
@@ -70,7 +71,7 @@ struct Chunk {
 
 // A workgroup takes blockDim chunks of one token; `splits` workgroups make up
 // a token.
-template <bool ROW_F32, bool OUT_F32, int KB>
+template <bool ROW_F32, bool OUT_F32, int KB, bool NT>
 __global__ __launch_bounds__(kCbThreads) void combine_kernel(CombineArgs a, int splits) {
   for (int64_t wg = blockIdx.x; wg < a.tokens * splits; wg += gridDim.x) {
     const int64_t t = wg / splits;
@@ -78,7 +79,7 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(CombineArgs a, int 
     const int32_t* slot = a.slot + t * a.top_k;
     const float* wt = a.weights + t * a.top_k;
     float acc[8];
-    Chunk<false> res;
+    Chunk<false, NT> res;
     if (a.residual) {
       res.load(row_buffer<false>(a.residual, t, a.tokens, a.n), c);
       res.get(acc);
@@ -87,7 +88,7 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(CombineArgs a, int 
       for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     }
     for (int j0 = 0; j0 < a.top_k; j0 += KB) {
-      Chunk<ROW_F32> r[KB];
+      Chunk<ROW_F32, NT> r[KB];
       int64_t s[KB];
 #pragma unroll
       for (int j = 0; j < KB; ++j) {
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(CombineArgs a, int 
         for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w, f[i], acc[i]);
       }
     }
-    Chunk<OUT_F32> y;
+    Chunk<OUT_F32, NT> y;
     y.set(acc);
     y.store(row_buffer<OUT_F32>(a.y, t, a.tokens, a.n), c);
   }
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(CombineArgs a, int 
 
 // One workgroup per token, KB choices at a time: dy is read once for all
 // of them, and their dot products are summed over the workgroup together.
-template <bool DY_F32, bool ROW_F32, int KB>
+template <bool DY_F32, bool ROW_F32, int KB, bool NT>
 __global__ __launch_bounds__(kCbBwdThreads) void combine_bwd_kernel(CombineBwdArgs a) {
   __shared__ float red[2][kCbBwdThreads / 64][KB];     // of this batch and the one before
   const int nch = (int)(a.n / 8), t = (int)threadIdx.x, threads = (int)blockDim.x;
@@ -131,8 +132,8 @@ __global__ __launch_bounds__(kCbBwdThreads) void combine_bwd_kernel(CombineBwdAr
         dot[j] = 0.f;
       }
       for (int c = t; c < nch; c += threads) {
-        Chunk<DY_F32> dy;
-        Chunk<ROW_F32> r[KB];
+        Chunk<DY_F32, NT> dy;
+        Chunk<ROW_F32, NT> r[KB];
         dy.load(dyb, c);
 #pragma unroll
         for (int j = 0; j < KB; ++j) r[j].load(rb[j], c);
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(kCbBwdThreads) void combine_bwd_kernel(CombineBwdAr
             dot[j] = __builtin_fmaf(d[i], f[i], dot[j]);
             g[i] = w[j] * d[i];
           }
-          Chunk<ROW_F32> o;
+          Chunk<ROW_F32, NT> o;
           o.set(g);
           o.store(db[j], c);
         }
@@ -174,51 +175,69 @@ int block_threads(int64_t n, int most) {
   return (int)((need + 63) / 64 * 64);
 }
 
-template <int KB>
+template <int KB, bool NT>
 void launch_combine_of(const CombineArgs& a, hipStream_t stream) {
   const int threads = a.n / 8 < kCbThreads ? block_threads(a.n, kCbThreads) : kCbThreads;
   const int splits = (int)((a.n / 8 + threads - 1) / threads);
   const int64_t wgs = a.tokens * splits;
   const dim3 grid((unsigned)(wgs < kMaxGrid ? wgs : kMaxGrid)), block((unsigned)threads);
   if (a.row_f32 && a.out_f32)
-    hipLaunchKernelGGL((combine_kernel<true, true, KB>), grid, block, 0, stream, a, splits);
+    hipLaunchKernelGGL((combine_kernel<true, true, KB, NT>), grid, block, 0, stream, a, splits);
   else if (a.row_f32)
-    hipLaunchKernelGGL((combine_kernel<true, false, KB>), grid, block, 0, stream, a, splits);
+    hipLaunchKernelGGL((combine_kernel<true, false, KB, NT>), grid, block, 0, stream, a, splits);
   else if (a.out_f32)
-    hipLaunchKernelGGL((combine_kernel<false, true, KB>), grid, block, 0, stream, a, splits);
+    hipLaunchKernelGGL((combine_kernel<false, true, KB, NT>), grid, block, 0, stream, a, splits);
   else
-    hipLaunchKernelGGL((combine_kernel<false, false, KB>), grid, block, 0, stream, a, splits);
+    hipLaunchKernelGGL((combine_kernel<false, false, KB, NT>), grid, block, 0, stream, a, splits);
 }
 
-template <int KB>
+template <int KB, bool NT>
 void launch_combine_bwd_of(const CombineBwdArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)(a.tokens < kMaxGrid ? a.tokens : kMaxGrid));
   const dim3 block((unsigned)block_threads(a.n, kCbBwdThreads));
   if (a.dy_f32 && a.row_f32)
-    hipLaunchKernelGGL((combine_bwd_kernel<true, true, KB>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((combine_bwd_kernel<true, true, KB, NT>), grid, block, 0, stream, a);
   else if (a.dy_f32)
-    hipLaunchKernelGGL((combine_bwd_kernel<true, false, KB>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((combine_bwd_kernel<true, false, KB, NT>), grid, block, 0, stream, a);
   else if (a.row_f32)
-    hipLaunchKernelGGL((combine_bwd_kernel<false, true, KB>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((combine_bwd_kernel<false, true, KB, NT>), grid, block, 0, stream, a);
   else
-    hipLaunchKernelGGL((combine_bwd_kernel<false, false, KB>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((combine_bwd_kernel<false, false, KB, NT>), grid, block, 0, stream, a);
+}
+
+template <bool NT>
+void launch_combine_nt(const CombineArgs& a, hipStream_t stream) {
+  if (a.top_k == 1) launch_combine_of<1, NT>(a, stream);
+  else if (a.top_k == 2) launch_combine_of<2, NT>(a, stream);
+  else if (a.top_k <= 4) launch_combine_of<4, NT>(a, stream);
+  else launch_combine_of<8, NT>(a, stream);
+}
+
+template <bool NT>
+void launch_combine_bwd_nt(const CombineBwdArgs& a, hipStream_t stream) {
+  if (a.top_k == 1) launch_combine_bwd_of<1, NT>(a, stream);
+  else if (a.top_k == 2) launch_combine_bwd_of<2, NT>(a, stream);
+  else if (a.top_k <= 4) launch_combine_bwd_of<4, NT>(a, stream);
+  else launch_combine_bwd_of<8, NT>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t stream) {
-  if (a.top_k == 1) launch_combine_of<1>(a, stream);
-  else if (a.top_k == 2) launch_combine_of<2>(a, stream);
-  else if (a.top_k <= 4) launch_combine_of<4>(a, stream);
-  else launch_combine_of<8>(a, stream);
+  const int64_t row = a.row_f32 ? 4 : 2, out = a.out_f32 ? 4 : 2, res = a.residual ? 2 : 0;
+  if (a.tokens * (a.top_k * row + out + res) > kCached / a.n)
+    launch_combine_nt<true>(a, stream);
+  else
+    launch_combine_nt<false>(a, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream) {
-  if (a.top_k == 1) launch_combine_bwd_of<1>(a, stream);
-  else if (a.top_k == 2) launch_combine_bwd_of<2>(a, stream);
-  else if (a.top_k <= 4) launch_combine_bwd_of<4>(a, stream);
-  else launch_combine_bwd_of<8>(a, stream);
+  const int64_t row = a.row_f32 ? 4 : 2, dy = a.dy_f32 ? 4 : 2;
+  if (a.n > 0 && a.tokens * (2 * a.top_k * row + dy) > kCached / a.n)
+    launch_combine_bwd_nt<true>(a, stream);
+  else
+    launch_combine_bwd_nt<false>(a, stream);
   return hipGetLastError();
 }
 

@@ -74,6 +74,15 @@ hipError_t launch_nvfp4_dequant(const uint8_t* q, const uint8_t* bs, const float
 // 2^32); kernels that take one row or token per workgroup walk on from there.
 constexpr int64_t kMaxGrid = int64_t(1) << 20;
 
+// Bytes of a call past which its accesses are nontemporal: what it reads and
+// writes does not stay in the 256 MB of the Infinity Cache anyway, and that
+// way its stores and loads disturb each other less.  16384 x 8 rows of 7168
+// combined: 412 us, 457 with the cache's own policy; norm of 16384 x 7168: 183
+// and 186, its gradient for 8192 x 7168: 91 and 96.  Smaller calls find their
+// inputs in the cache and leave their outputs there (a thousand rows of 5152,
+// normed: 8.7 us, nontemporal 9.4).
+constexpr int64_t kCached = int64_t(256) << 20;
+
 struct RmsNorm {
   const uint16_t* x;
   const uint16_t* residual;

@@ -12,8 +12,7 @@
 // of the row in registers between the sum of squares and the encode, so the
 // row is read once; a 1x128 tile is 16 adjacent lanes, a 1x32 block 4.  Bound
 // by HBM for many rows: 16384 x 7168 with residual, h and y, 9 bytes per
-// element, in 186 us (5.7 TB/s; nontemporal accesses 183 us, but 9.4 against
-// 8.7 us for a thousand rows).  A few rows are bound by latency: 4.1 us.
+// element, in 183 us (5.8 TB/s).  A few rows are bound by latency: 3.9 us.
 #include "device.h"
 #include "launch.h"
 
@@ -45,6 +44,21 @@ __device__ __forceinline__ void unpack8(const u32x4& v, float* f) {
 
 __device__ __forceinline__ u32x4 pack8(const float* f) {
   return (u32x4){pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+}
+
+template <bool NT>
+__device__ __forceinline__ u32x4 load(const u32x4* p) {
+  if constexpr (NT)
+    return __builtin_nontemporal_load(p);
+  else
+    return *p;
+}
+template <bool NT, typename T>
+__device__ __forceinline__ void store(T v, T* p) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
 }
 
 // Weights of chunk c as fp32.
@@ -91,7 +105,7 @@ __device__ __forceinline__ uint32_t e8m0_code_f32(uint32_t bits) {
 }
 
 // BLK 32 or 128; CH chunks per thread.
-template <int BLK, bool FLOOR, bool WF32, int CH>
+template <int BLK, bool FLOOR, bool WF32, int CH, bool NT>
 __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormParams p) {
   __shared__ float red[2][2][16];         // of this row and the one before, the sum and the rescaled one
   const int T = (int)blockDim.x, t = (int)threadIdx.x;
@@ -105,15 +119,15 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormParams p) {
     const int c = t + i * T;
     u32x4 v = {0u, 0u, 0u, 0u};
     if (c < p.nch) {
-      v = p.x[base + c];
+      v = load<NT>(p.x + base + c);
       if (p.res) {
         float a[8], b[8];
         unpack8(v, a);
-        unpack8(p.res[base + c], b);
+        unpack8(load<NT>(p.res + base + c), b);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] += b[j];
         v = pack8(a);
-        p.h[base + c] = v;
+        store<NT>(v, p.h + base + c);
       }
     }
     unpack8(v, f[i]);
@@ -180,15 +194,15 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormParams p) {
       u32x2 cc;
       cc.x = cvt4_e4m3(v[0], v[1], v[2], v[3]);
       cc.y = cvt4_e4m3(v[4], v[5], v[6], v[7]);
-      p.q[base + c] = cc;
-      if (p.y) p.y[base + c] = pack8(f[i]);
+      store<NT>(cc, p.q + base + c);
+      if (p.y) store<NT>(pack8(f[i]), p.y + base + c);
       if (p.ydq) {
         float d[8];
         decode4_e4m3(cc.x, d);
         decode4_e4m3(cc.y, d + 4);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] *= sval;
-        p.ydq[base + c] = pack8(d);
+        store<NT>(pack8(d), p.ydq + base + c);
       }
       if ((t & (BLK / 8 - 1)) == 0) {
         if constexpr (BLK == 128)
@@ -216,11 +230,11 @@ struct NormBwdParams {
 
 // Workgroup b takes the rows b, b + G, ...; the weight gradient of its rows
 // stays in registers and goes to the workspace once.  Bound by reading dy, h
-// and dres and writing dx: 8192 x 7168 in 88 us (5.3 TB/s) and 4 us for the
-// partials (two launches replayed: 96 us).  Two rows at a time, rows kept packed across the barrier and
-// dres loaded before it all took registers that cost a workgroup per CU, and
-// 10 to 60% more time.
-template <bool WF32, int CH>
+// and dres and writing dx: 8192 x 7168 in 91 us with the partials' sum (5.1
+// TB/s).  Two rows at a time, rows kept packed across the barrier and dres
+// loaded before it all took registers that cost a workgroup per CU, and 10 to
+// 60% more time.
+template <bool WF32, int CH, bool NT>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
   __shared__ float red[2][16];            // of this row and the one before
   const int T = (int)blockDim.x, t = (int)threadIdx.x;
@@ -241,8 +255,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
       const bool in = c < p.nch;
       u32x4 a = {0u, 0u, 0u, 0u}, b = {0u, 0u, 0u, 0u};
       if (in) {
-        a = p.h[base + c];
-        b = p.dy[base + c];
+        a = load<NT>(p.h + base + c);
+        b = load<NT>(p.dy + base + c);
       }
       float w[8];
       load_weight8<WF32>(p.w, in ? c : 0, w);
@@ -266,11 +280,11 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
       for (int j = 0; j < 8; ++j) d[j] = rstd * __builtin_fmaf(-xh[i][j], c1, wd[i][j]);
       if (p.dres) {
         float r[8];
-        unpack8(p.dres[base + c], r);
+        unpack8(load<NT>(p.dres + base + c), r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] += r[j];
       }
-      p.dx[base + c] = pack8(d);
+      store<NT>(pack8(d), p.dx + base + c);
     }
   }
   v4f* out = reinterpret_cast<v4f*>(p.part) + (int64_t)blockIdx.x * p.nch * 2;
@@ -352,8 +366,13 @@ hipError_t launch_rmsnorm_quant(const RmsNorm& a, hipStream_t stream) {
                (float)a.cols, a.eps, reinterpret_cast<u32x2*>(a.q), a.scale, reinterpret_cast<u32x4*>(a.h),
                reinterpret_cast<u32x4*>(a.y), reinterpret_cast<u32x4*>(a.ydq), a.rstd, a.rows};
   const dim3 grid((unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid)), block((unsigned)threads);
-#define FP8BLK_NORM(B, F, W, C) \
-  hipLaunchKernelGGL((rmsnorm_quant_kernel<B, F, W, C>), grid, block, 0, stream, p)
+  const int64_t bytes = (a.residual ? 6 : 2) + 1 + (a.y ? 2 : 0) + (a.ydq ? 2 : 0);       // per element
+  const bool nt = a.rows * a.cols * bytes > kCached;
+#define FP8BLK_NORM(B, F, W, C)                                                                      \
+  do {                                                                                               \
+    if (nt) hipLaunchKernelGGL((rmsnorm_quant_kernel<B, F, W, C, true>), grid, block, 0, stream, p); \
+    else hipLaunchKernelGGL((rmsnorm_quant_kernel<B, F, W, C, false>), grid, block, 0, stream, p);   \
+  } while (0)
 #define FP8BLK_NORM_CH(B, F, W)                     \
   do {                                              \
     if (ch == 1) FP8BLK_NORM(B, F, W, 1);           \
@@ -386,7 +405,12 @@ hipError_t launch_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const void*
     NormBwdParams p{reinterpret_cast<const u32x4*>(dy), reinterpret_cast<const u32x4*>(h), w, rstd,
                     reinterpret_cast<const u32x4*>(dres), rows, nch, (float)cols, reinterpret_cast<u32x4*>(dx), part};
     const dim3 grid((unsigned)parts), block((unsigned)threads);
-#define FP8BLK_NB(W, C) hipLaunchKernelGGL((rmsnorm_bwd_kernel<W, C>), grid, block, 0, stream, p)
+    const bool nt = rows * cols * (dres ? 8 : 6) > kCached;
+#define FP8BLK_NB(W, C)                                                                      \
+  do {                                                                                       \
+    if (nt) hipLaunchKernelGGL((rmsnorm_bwd_kernel<W, C, true>), grid, block, 0, stream, p); \
+    else hipLaunchKernelGGL((rmsnorm_bwd_kernel<W, C, false>), grid, block, 0, stream, p);   \
+  } while (0)
     if (w_f32) {
       if (ch == 1) FP8BLK_NB(true, 1);
       else if (ch == 2) FP8BLK_NB(true, 2);

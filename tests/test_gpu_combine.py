@@ -104,6 +104,34 @@ def test_rows_beyond_32_bit_offsets():
     assert dw[0, 1] == 0 and dw[1, 0] == 0
 
 
+@pytest.mark.parametrize("row_dtype", [BF, F32])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("top_k", [1, 2, 3, 8])
+def test_a_large_call_is_its_small_ones(row_dtype, out_dtype, top_k):
+    """Calls past the size of the last cache (nontemporal) against the same tokens in calls below it."""
+    n, tokens = 4104, 36000 // top_k + 3
+    g = torch.Generator("cuda").manual_seed(top_k)
+    rows = torch.randn((tokens * top_k, n), device="cuda", generator=g).to(row_dtype)
+    res = torch.randn((tokens, n), device="cuda", generator=g).to(BF)
+    slot = torch.randperm(tokens * top_k, device="cuda", generator=g).to(torch.int32).view(tokens, top_k)
+    w = torch.rand((tokens, top_k), device="cuda", generator=g)
+    y = fb.moe_combine(rows, slot, w, residual=res, out_dtype=out_dtype)
+    dy = res if out_dtype == BF else res.float()
+    drows, dw = fb.moe_combine_backward(dy, rows, slot, w)
+    parts = torch.empty_like(rows)
+    step = tokens // 12
+    for t in range(0, tokens, step):
+        cut = slice(t, min(t + step, tokens))
+        one = fb.moe_combine(rows, slot[cut].contiguous(), w[cut].contiguous(), residual=res[cut].contiguous(),
+                             out_dtype=out_dtype)
+        assert torch.equal(y[cut], one)
+        dwc = torch.empty_like(w[cut])
+        fb.fp8_moe_combine_backward(dy[cut].contiguous(), rows, slot[cut].contiguous(), w[cut].contiguous(), parts,
+                                    dwc)
+        assert torch.equal(dw[cut], dwc)
+    assert torch.equal(drows, parts)
+
+
 @pytest.mark.parametrize("tokens,top_k,n,total", SHAPES)
 @pytest.mark.parametrize("row_dtype", [BF, F32])
 @pytest.mark.parametrize("dy_dtype", [BF, F32])

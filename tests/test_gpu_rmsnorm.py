@@ -169,6 +169,31 @@ def test_rows_beyond_32_bit_offsets():
     assert torch.all((dw - dw2).abs() <= 2.0 ** -22 * dw2.abs())          # three rows, added in another order
 
 
+@pytest.mark.parametrize("block", ["1x32", "1x128"])
+@pytest.mark.parametrize("cols", [1152, 7168, 16384, 20480])
+def test_a_large_call_is_its_small_ones(block, cols):
+    """Calls past the size of the last cache (nontemporal) against the same rows in calls below it."""
+    rows = 80_000_000 // cols + 3
+    g = torch.Generator("cuda").manual_seed(cols)
+    x, r = (torch.randn((rows, cols), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    w = torch.rand(cols, device="cuda", generator=g) + 0.5
+    whole = fb.rmsnorm_quantize(x, w, EPS, residual=r, block=block, normed=True, dequant=True, save_rstd=True)
+    dx, dw = fb.rmsnorm_backward(r, whole["h"], w, whole["rstd"], dres=x)
+    total, mag = torch.zeros_like(w).double(), torch.zeros_like(w).double()
+    step = rows // 8
+    for t in range(0, rows, step):
+        cut = slice(t, min(t + step, rows))
+        one = fb.rmsnorm_quantize(x[cut].contiguous(), w, EPS, residual=r[cut].contiguous(), block=block, normed=True,
+                                  dequant=True, save_rstd=True)
+        for name, v in one.items():
+            assert torch.equal(whole[name][cut].view(torch.uint8), v.view(torch.uint8)), name
+        dxc, dwc = fb.rmsnorm_backward(r[cut].contiguous(), one["h"], w, one["rstd"], dres=x[cut].contiguous())
+        assert torch.equal(dx[cut], dxc)
+        total += dwc.double()
+        mag += (r[cut].float() * one["h"].float() * one["rstd"][:, None]).abs().sum(0, dtype=torch.float64)
+    assert torch.all((dw.double() - total).abs() <= 2.0 ** -14 * mag)     # both sums of up to 2^9 additions
+
+
 def test_same_bytes_every_time():
     rng = np.random.default_rng(19)
     h, dy = (bf16_from_bits(_values(rng, 3000, 1152, "normal")) for _ in range(2))
