@@ -16,7 +16,7 @@
 //     row, v_dot2_f32_bf16 on the unscaled values of a block and one fused
 //     multiply by its scale: 1.7 instructions per weight at two rows, no
 //     LDS.  Taken for groups of at most two rows on large grids: 64 rows on
-//     52 experts of 4096 x 7168 in 159 us (5.4 TB/s), against 165 us on the
+//     52 experts of 4096 x 7168 in 153 us (5.6 TB/s), against 185 us on the
 //     matrix cores; on grids of up to 256 tiles it was 7% slower at two rows.
 #include "device.h"
 #include "launch.h"
@@ -92,6 +92,12 @@ __device__ __forceinline__ Buffer make_buffer(const void* base, uint32_t bytes) 
 __device__ __forceinline__ u32x4 load16(Buffer b, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0);
 }
+// Codes of weights: NT, with the nontemporal bit (scales are read 32 bytes of
+// a line at a time, and keep theirs).
+template <bool NT>
+__device__ __forceinline__ u32x4 load_codes(Buffer b, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, NT ? 2 : 0);
+}
 
 // One run of 32 weights: a lane's share of a step of dot_rows.
 struct Run {
@@ -113,7 +119,7 @@ __device__ __forceinline__ void store_y(const MatvecArgs& a, int grp, int64_t ro
 // is 512 k, 256 bytes of a row per 16 lanes), the next step's loads in
 // flight during the products of this one.
 constexpr int kDotQ = 8;
-template <bool OUT_F32>
+template <bool NT, bool OUT_F32>
 __device__ __forceinline__ void dot_rows(const MatvecArgs& a, int grp, int lo, int rows, int64_t n0, int lane) {
   constexpr int Q = kDotQ, M = 2;
   const int kl = lane & 15, sub = lane >> 4;
@@ -147,7 +153,7 @@ __device__ __forceinline__ void dot_rows(const MatvecArgs& a, int grp, int lo, i
       for (int i = 0; i < 4; ++i) x[m][i] = load16(xb, ((x0[m] + (uint32_t)s * 1024) | skip) + 16 * i);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      c[q].c = load16(qb, (q0 + (uint32_t)(q * 2 * K + s * 256)) | skip);
+      c[q].c = load_codes<NT>(qb, (q0 + (uint32_t)(q * 2 * K + s * 256)) | skip);
       c[q].s = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(sb, (s0 + (uint32_t)(q * (K / 4) + s * 32)) | skip, 0, 0);
     }
   };
@@ -225,7 +231,7 @@ struct Stage {
 // both sides.  The next step's loads are in flight (in registers) while this
 // one is multiplied from LDS.  AL: k % 64 == 0 and buffers aligned so that a
 // lane's codes are 16 aligned bytes and its scales a dword.
-template <bool AL, int R, int MX, int KS, bool OUT_F32>
+template <bool AL, int R, int MX, int KS, bool NT, bool OUT_F32>
 __device__ __forceinline__ void mfma_rows(const MatvecArgs& a, int grp, int lo, int hi, int64_t n0, uint8_t* smem,
                                           int t, int wave) {
   using S = Stage<R, MX>;
@@ -274,7 +280,7 @@ __device__ __forceinline__ void mfma_rows(const MatvecArgs& a, int grp, int lo, 
         for (int h = 0; h < 2; ++h) {
           const uint32_t o = qo + (uint32_t)((16 * r + 8 * h) * (K / 2));
           if constexpr (AL) {
-            cq[r][h] = load16(qb, o | (kc < K ? 0u : kNoLoad));
+            cq[r][h] = load_codes<NT>(qb, o | (kc < K ? 0u : kNoLoad));
           } else {
             const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(qb, o | (kc < K ? 0u : kNoLoad), 0, 0);
             const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(qb, (o + 8) | (kc + 16 < K ? 0u : kNoLoad), 0, 0);
@@ -370,7 +376,7 @@ __device__ __forceinline__ void mfma_rows(const MatvecArgs& a, int grp, int lo, 
   }
 }
 
-template <bool AL, int R, int MX, int KS, bool OUT_F32>
+template <bool AL, int R, int MX, int KS, bool NT, bool OUT_F32>
 __global__ __launch_bounds__(64 * KS) void matvec_kernel(MatvecArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[KS * Stage<R, MX>::kBytes];
   const int t = (int)threadIdx.x;
@@ -381,13 +387,13 @@ __global__ __launch_bounds__(64 * KS) void matvec_kernel(MatvecArgs a) {
     lo = (int)(blockIdx.y * a.slice);
     hi = lo + (int)a.slice < (int)a.total_m ? lo + (int)a.slice : (int)a.total_m;
   }
-  mfma_rows<AL, R, MX, KS, OUT_F32>(a, grp, lo, hi, (int64_t)blockIdx.x * (16 * R), smem, t,
+  mfma_rows<AL, R, MX, KS, NT, OUT_F32>(a, grp, lo, hi, (int64_t)blockIdx.x * (16 * R), smem, t,
                                     __builtin_amdgcn_readfirstlane(t >> 6));
 }
 
 // One wave per 32 weight rows; the matrix cores for groups of more than two
 // rows, which a skewed routing has among its small ones.
-template <bool OUT_F32>
+template <bool NT, bool OUT_F32>
 __global__ __launch_bounds__(64) void matvec_stream_kernel(MatvecArgs a) {
   static_assert(4 * kDotQ == 16 * 2, "both ways take 32 weight rows");
   __shared__ __attribute__((aligned(16))) uint8_t smem[Stage<2, 16>::kBytes];
@@ -396,18 +402,27 @@ __global__ __launch_bounds__(64) void matvec_stream_kernel(MatvecArgs a) {
   if (a.offsets && !nth_group(a, (int)blockIdx.y, t, &grp, &lo, &hi)) return;
   const int64_t n0 = (int64_t)blockIdx.x * 32;
   if (hi - lo <= 2)
-    dot_rows<OUT_F32>(a, grp, lo, hi - lo, n0, t);
+    dot_rows<NT, OUT_F32>(a, grp, lo, hi - lo, n0, t);
   else
-    mfma_rows<true, 2, 16, 1, OUT_F32>(a, grp, lo, hi, n0, smem, t, 0);
+    mfma_rows<true, 2, 16, 1, NT, OUT_F32>(a, grp, lo, hi, n0, smem, t, 0);
 }
 
-template <bool AL, int R, int MX, int KS>
+template <bool AL, int R, int MX, int KS, bool NT = false>
 void launch_tiles(const MatvecArgs& a, int64_t slices, hipStream_t stream) {
   const dim3 grid((unsigned)((a.n + 16 * R - 1) / (16 * R)), (unsigned)slices);
   if (a.out_f32)
-    hipLaunchKernelGGL((matvec_kernel<AL, R, MX, KS, true>), grid, dim3(64 * KS), 0, stream, a);
+    hipLaunchKernelGGL((matvec_kernel<AL, R, MX, KS, NT, true>), grid, dim3(64 * KS), 0, stream, a);
   else
-    hipLaunchKernelGGL((matvec_kernel<AL, R, MX, KS, false>), grid, dim3(64 * KS), 0, stream, a);
+    hipLaunchKernelGGL((matvec_kernel<AL, R, MX, KS, NT, false>), grid, dim3(64 * KS), 0, stream, a);
+}
+
+template <bool NT>
+void launch_stream(const MatvecArgs& a, int64_t active, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.n + 31) / 32), (unsigned)active);
+  if (a.out_f32)
+    hipLaunchKernelGGL((matvec_stream_kernel<NT, true>), grid, dim3(64), 0, stream, a);
+  else
+    hipLaunchKernelGGL((matvec_stream_kernel<NT, false>), grid, dim3(64), 0, stream, a);
 }
 
 // Rows of x per pass, tiles per workgroup and waves that share k.  tiles:
@@ -423,7 +438,7 @@ void launch_tiles(const MatvecArgs& a, int64_t slices, hipStream_t stream) {
 // except for groups, of which one may have many more rows than the others;
 // two steps in flight, or half a tile per workgroup, gained nothing.
 template <bool AL>
-void launch_rows(const MatvecArgs& a, int64_t slices, int64_t tiles, int64_t rows, hipStream_t stream) {
+void launch_rows(const MatvecArgs& a, int64_t slices, int64_t tiles, int64_t rows, bool nt, hipStream_t stream) {
   if (rows <= 2 && !a.offsets) {
     if (tiles <= 256)
       launch_tiles<AL, 1, 2, 8>(a, slices, stream);
@@ -438,6 +453,8 @@ void launch_rows(const MatvecArgs& a, int64_t slices, int64_t tiles, int64_t row
       launch_tiles<AL, 1, 16, 8>(a, slices, stream);
     else if (tiles <= 1024)
       launch_tiles<AL, 2, 16, 4>(a, slices, stream);
+    else if (AL && nt)
+      launch_tiles<AL, 4, 16, 4, AL>(a, slices, stream);
     else
       launch_tiles<AL, 4, 16, 4>(a, slices, stream);
   } else {
@@ -445,6 +462,8 @@ void launch_rows(const MatvecArgs& a, int64_t slices, int64_t tiles, int64_t row
       launch_tiles<AL, 1, 32, 8>(a, slices, stream);
     else if (tiles <= 1024)
       launch_tiles<AL, 2, 32, 4>(a, slices, stream);
+    else if (AL && nt)
+      launch_tiles<AL, 4, 32, 2, AL>(a, slices, stream);
     else
       launch_tiles<AL, 4, 32, 2>(a, slices, stream);
   }
@@ -471,16 +490,16 @@ hipError_t launch_matvec(const MatvecArgs& args, hipStream_t stream) {
     a.slice = rows = (a.total_m + most - 1) / most;
     slices = (a.total_m + rows - 1) / rows;
   }
+  const bool nt = al && tiles > 1024 && active * a.n * (a.k / 2) > kCached;
   if (al && rows <= 2 && tiles > 1024) {
-    const dim3 grid((unsigned)((a.n + 31) / 32), (unsigned)active);
-    if (a.out_f32)
-      hipLaunchKernelGGL(matvec_stream_kernel<true>, grid, dim3(64), 0, stream, a);
+    if (nt)
+      launch_stream<true>(a, active, stream);
     else
-      hipLaunchKernelGGL(matvec_stream_kernel<false>, grid, dim3(64), 0, stream, a);
+      launch_stream<false>(a, active, stream);
   } else if (al) {
-    launch_rows<true>(a, slices, tiles, rows, stream);
+    launch_rows<true>(a, slices, tiles, rows, nt, stream);
   } else {
-    launch_rows<false>(a, slices, tiles, rows, stream);
+    launch_rows<false>(a, slices, tiles, rows, nt, stream);
   }
   return hipGetLastError();
 }

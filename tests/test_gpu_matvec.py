@@ -202,3 +202,36 @@ def test_weights_beyond_32_bit_offsets():
     y = fb.nvfp4_grouped_matvec(bf16_from_bits(f32_to_bf16(x.astype(np.float32))), q, bs, torch.ones(g, device="cuda"),
                                 off, out_dtype=torch.float32)
     assert np.array_equal(_out(y), x @ moe.nvfp4_matrix(qn, bn, [1.0], n).T)
+
+
+@pytest.mark.parametrize("sizes", [[2, 1, 0, 2] * 10, [0, 9, 1, 2] * 10, [30, 10, 17, 5] * 10, [7] * 40])
+def test_a_large_call_is_its_small_ones(sizes):
+    """Weights past the size of the last cache (nontemporal) against the same groups one by one, in exact sums."""
+    n, k = 4096, 4096
+    g = torch.Generator("cuda").manual_seed(sum(sizes))
+    q = torch.randint(0, 256, (len(sizes), n, k // 2), dtype=torch.uint8, device="cuda", generator=g)
+    bs = torch.full((len(sizes), n, k // 16), 0x38, dtype=torch.uint8, device="cuda")
+    gs = torch.full((len(sizes),), 0.5, device="cuda")
+    x = torch.randint(-8, 9, (sum(sizes), k), device="cuda", generator=g).to(torch.bfloat16)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        y = fb.nvfp4_grouped_matvec(x, q, bs, gs, off, out_dtype=dtype)
+        at = 0
+        for e, rows in enumerate(sizes):
+            one = fb.nvfp4_matvec(x[at:at + rows], q[e], bs[e], gs[e:e + 1], out_dtype=dtype)
+            assert torch.equal(y[at:at + rows], one), (e, rows)
+            at += rows
+
+
+@pytest.mark.parametrize("m", [1, 2, 5, 20])
+def test_a_large_matrix_is_its_rows(m):
+    n, k = 80000, 7168
+    g = torch.Generator("cuda").manual_seed(m)
+    q = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device="cuda", generator=g)
+    bs = torch.full((n, k // 16), 0x38, dtype=torch.uint8, device="cuda")
+    gs = torch.full((1,), 0.5, device="cuda")
+    x = torch.randint(-8, 9, (m, k), device="cuda", generator=g).to(torch.bfloat16)
+    y = fb.nvfp4_matvec(x, q, bs, gs, out_dtype=torch.float32)
+    for j in range(0, n, 10000):
+        one = fb.nvfp4_matvec(x, q[j:j + 10000], bs[j:j + 10000], gs, out_dtype=torch.float32)
+        assert torch.equal(y[:, j:j + 10000], one)
