@@ -297,32 +297,39 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
   }
 }
 
-// Sum of the partial weight gradients: 16 columns per workgroup, 64 threads
-// to a column (thread q takes the partials q, q + 64, ...), added as a tree.
+// Sum of the partial weight gradients: 32 columns per workgroup (128 bytes of
+// a partial), 64 threads to four of them (thread q takes the partials q, q +
+// 64, ...), added in LDS as a tree.
 template <bool WF32>
-__global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* __restrict__ part, int parts, int cols,
-                                                          void* __restrict__ dw) {
-  __shared__ float red[64][17];
-  const int lane = (int)(threadIdx.x & 15), q = (int)(threadIdx.x >> 4);
-  const int col = (int)blockIdx.x * 16 + lane;
-  float s = 0.f;
-  if (col < cols)
+__global__ __launch_bounds__(512) void rmsnorm_dw_kernel(const v4f* __restrict__ part, int parts, int cols,
+                                                         void* __restrict__ dw) {
+  __shared__ v4f red[64][9];
+  const int lane = (int)(threadIdx.x & 7), q = (int)(threadIdx.x >> 3);
+  const int c4 = (int)blockIdx.x * 8 + lane;
+  v4f s = {0.f, 0.f, 0.f, 0.f};
+  if (c4 * 4 < cols)
 #pragma unroll 8
-    for (int i = q; i < parts; i += 64) s += part[(int64_t)i * cols + col];
+    for (int i = q; i < parts; i += 64) s += part[(int64_t)i * (cols / 4) + c4];
   red[q][lane] = s;
   __syncthreads();
-  if (threadIdx.x < 16 * 4) {
-    s = 0.f;
+  if (threadIdx.x >= 64) return;
+  s = red[q][lane];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += red[q * 16 + i][lane];
-    s += __shfl_xor(s, 16, 64);
-    s += __shfl_xor(s, 32, 64);
-    if (q == 0 && col < cols) {
-      if constexpr (WF32)
-        reinterpret_cast<float*>(dw)[col] = s;
-      else
-        reinterpret_cast<uint16_t*>(dw)[col] = (uint16_t)pack_bf16x2(s, 0.f);
-    }
+  for (int i = 8; i < 64; i += 8) s += red[q + i][lane];
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  red[q][lane] = s;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  if (threadIdx.x >= 8 || c4 * 4 >= cols) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s += red[i][lane];
+  if constexpr (WF32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<float*>(dw)[c4 * 4 + i] = s[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint16_t*>(dw)[c4 * 4 + i] = (uint16_t)pack_bf16x2(s[i], 0.f);
   }
 }
 
@@ -398,12 +405,13 @@ hipError_t launch_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const void*
                               void* dw, hipStream_t stream) {
   const int nch = (int)(cols / 8);
   const int parts = (int)rmsnorm_bwd_parts(rows, cols);
-  float* part = reinterpret_cast<float*>(workspace);
+  v4f* part = reinterpret_cast<v4f*>(workspace);
   if (rows > 0) {
     int ch, threads;
     row_shape(nch, 0, &ch, &threads);
     NormBwdParams p{reinterpret_cast<const u32x4*>(dy), reinterpret_cast<const u32x4*>(h), w, rstd,
-                    reinterpret_cast<const u32x4*>(dres), rows, nch, (float)cols, reinterpret_cast<u32x4*>(dx), part};
+                    reinterpret_cast<const u32x4*>(dres), rows, nch, (float)cols, reinterpret_cast<u32x4*>(dx),
+                    reinterpret_cast<float*>(part)};
     const dim3 grid((unsigned)parts), block((unsigned)threads);
     const bool nt = rows * cols * (dres ? 8 : 6) > kCached;
 #define FP8BLK_NB(W, C)                                                                      \
@@ -422,11 +430,11 @@ hipError_t launch_rmsnorm_bwd(const uint16_t* dy, const uint16_t* h, const void*
     }
 #undef FP8BLK_NB
   }
-  const dim3 grid((unsigned)((cols + 15) / 16));
+  const dim3 grid((unsigned)((cols + 31) / 32));
   if (w_f32)
-    hipLaunchKernelGGL(rmsnorm_dw_kernel<true>, grid, dim3(1024), 0, stream, part, parts, (int)cols, dw);
+    hipLaunchKernelGGL(rmsnorm_dw_kernel<true>, grid, dim3(512), 0, stream, part, parts, (int)cols, dw);
   else
-    hipLaunchKernelGGL(rmsnorm_dw_kernel<false>, grid, dim3(1024), 0, stream, part, parts, (int)cols, dw);
+    hipLaunchKernelGGL(rmsnorm_dw_kernel<false>, grid, dim3(512), 0, stream, part, parts, (int)cols, dw);
   return hipGetLastError();
 }
 
