@@ -230,12 +230,15 @@ struct NormBwdParams {
 
 // Workgroup b takes the rows b, b + G, ...; the weight gradient of its rows
 // stays in registers and goes to the workspace once.  Bound by reading dy, h
-// and dres and writing dx: 8192 x 7168 in 91 us with the partials' sum (5.1
-// TB/s).  Two rows at a time, rows kept packed across the barrier and dres
+// and dres and writing dx: 8192 x 7168 in 89 us with the partials' sum (5.3
+// TB/s).  Rows wider than 16384 are read twice (the second time from the L2):
+// kept in registers they spill, 2048 x 32768 in 233 us instead of 161.  Two
+// rows at a time, rows kept packed across the barrier and dres
 // loaded before it all took registers that cost a workgroup per CU, and 10 to
 // 60% more time.
 template <bool WF32, int CH, bool NT>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
+  constexpr bool KEEP = CH < 4;           // a row's chunks fit the registers
   __shared__ float red[2][16];            // of this row and the one before
   const int T = (int)blockDim.x, t = (int)threadIdx.x;
   int turn = 0;
@@ -247,37 +250,50 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
     const int64_t base = row * p.nch;
     const float rstd = p.rstd[row];
-    float xh[CH][8], wd[CH][8];
+    float xh[KEEP ? CH : 1][8], wd[KEEP ? CH : 1][8];
     float dot = 0.f;
+    // chunk i's xh into x and dy into d
+    auto read = [&](int i, float* x, float* d) {
+      const int c = t + i * T;
+      u32x4 a = {0u, 0u, 0u, 0u}, b = {0u, 0u, 0u, 0u};
+      if (c < p.nch) {
+        a = load<NT && KEEP>(p.h + base + c);
+        b = load<NT && KEEP>(p.dy + base + c);
+      }
+      unpack8(a, x);
+      unpack8(b, d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= rstd;
+    };
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = t + i * T;
-      const bool in = c < p.nch;
-      u32x4 a = {0u, 0u, 0u, 0u}, b = {0u, 0u, 0u, 0u};
-      if (in) {
-        a = load<NT>(p.h + base + c);
-        b = load<NT>(p.dy + base + c);
-      }
+      const int c = t + i * T, at = KEEP ? i : 0;
+      read(i, xh[at], wd[at]);
       float w[8];
-      load_weight8<WF32>(p.w, in ? c : 0, w);
-      unpack8(a, xh[i]);
-      unpack8(b, wd[i]);
+      load_weight8<WF32>(p.w, c < p.nch ? c : 0, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        xh[i][j] *= rstd;
-        acc[i][j] = __builtin_fmaf(wd[i][j], xh[i][j], acc[i][j]);
-        wd[i][j] *= w[j];
-        dot = __builtin_fmaf(wd[i][j], xh[i][j], dot);
+        acc[i][j] = __builtin_fmaf(wd[at][j], xh[at][j], acc[i][j]);
+        wd[at][j] *= w[j];
+        dot = __builtin_fmaf(wd[at][j], xh[at][j], dot);
       }
+      if constexpr (!KEEP) __builtin_amdgcn_sched_barrier(0);     // one chunk in registers at a time
     }
     const float c1 = block_sum(dot, red[turn]) / p.cols;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = t + i * T;
+      const int c = t + i * T, at = KEEP ? i : 0;
       if (c >= p.nch) continue;
+      if constexpr (!KEEP) {
+        read(i, xh[at], wd[at]);
+        float w[8];
+        load_weight8<WF32>(p.w, c, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wd[at][j] *= w[j];
+      }
       float d[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = rstd * __builtin_fmaf(-xh[i][j], c1, wd[i][j]);
+      for (int j = 0; j < 8; ++j) d[j] = rstd * __builtin_fmaf(-xh[at][j], c1, wd[at][j]);
       if (p.dres) {
         float r[8];
         unpack8(load<NT>(p.dres + base + c), r);
