@@ -809,12 +809,13 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
     const bool ok = id[k] >= 0 && id[k] < E;
     // lanes of the wave with the same expert
     unsigned long long same = __builtin_amdgcn_ballot_w64(ok);
+    rank[k] = -1;
+    if (same == 0) continue;
     for (int b = 0; b < bits; ++b) {
       const bool one = (id[k] >> b) & 1;
       const unsigned long long set = __builtin_amdgcn_ballot_w64(one);
       same &= one ? set : ~set;
     }
-    rank[k] = -1;
     if (ok) {
       rank[k] = ctr[id[k]] + __builtin_popcountll(same & ((1ull << lane) - 1));
       // the last of them moves the counter on (after every lane has read it)
