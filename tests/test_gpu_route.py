@@ -238,6 +238,16 @@ def test_backward_of_left_out_repeated_and_masked(score, renorm):
     assert np.all(got[2] == 0) and np.all(got[5] == 0) and got[4, 3] == 0
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_one_renormalized_choice_has_no_gradient(score):
+    """Its weight is the scale whatever the logits: zeros, not the rounding of a difference."""
+    l, _ = _logits(np.random.default_rng(41), 300, 75, torch.float32)
+    ids, w = fb.moe_route(l, 1, score=score, renorm=True, scale=2.5)
+    assert torch.all(w == 2.5)
+    d = fb.moe_route_backward(l, ids, torch.randn((300, 1), device="cuda"), score=score, renorm=True, scale=2.5)
+    assert torch.all(d == 0)
+
+
 def test_more_tokens_than_one_launch_takes():
     """Tokens past the largest grid of a launch; 32 tokens of 8 experts to a workgroup."""
     tokens = 32 * (1 << 20) + 37
