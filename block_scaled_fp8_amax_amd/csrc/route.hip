@@ -401,7 +401,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int vec, int64_
   const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
   const int gl = lane & (G - 1), sub = lane / G;
   const float none = -__builtin_inff();
-  const int E = a.experts, per = a.per;
+  const int E = a.experts;
   // per wave: 64 EPL keys (floats, or doubles where it chooses again), TPW * 64 choices
   constexpr int kKeyBytes = 64 * EPL * 8;
   uint8_t* mine = reinterpret_cast<uint8_t*>(smem) + wave * (kKeyBytes + TPW * 256);
@@ -682,7 +682,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a, int vec,
   if (vec) {
 #pragma unroll
     for (int i = 0; i < EPL; i += 4) {
-      if (e0 + i >= E) break;
+      if (e0 + i >= E) continue;
       if (a.logits_f32) {
         *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.dlogits) + t * E + e0 + i) =
             (v4f){d[i], d[i + 1], d[i + 2], d[i + 3]};
@@ -694,7 +694,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a, int vec,
   } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      if (e0 + i >= E) break;
+      if (e0 + i >= E) continue;
       if (a.logits_f32)
         reinterpret_cast<float*>(a.dlogits)[t * E + e0 + i] = d[i];
       else

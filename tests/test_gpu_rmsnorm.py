@@ -154,6 +154,19 @@ def test_h_written_over_x():
     assert torch.equal(s, want["scale"])
 
 
+@pytest.mark.parametrize("over", ["dy", "dres"])
+@pytest.mark.parametrize("rows,cols", [(700, 1152), (300, 12288), (300, 20480), (6000, 7168)])
+def test_dx_written_over_an_input(over, rows, cols):
+    g = torch.Generator("cuda").manual_seed(rows + cols)
+    h, dy, dres = (torch.randn((rows, cols), device="cuda", generator=g).to(torch.bfloat16) for _ in range(3))
+    w, r = torch.rand(cols, device="cuda", generator=g), torch.rand(rows, device="cuda", generator=g)
+    want, dw = fb.rmsnorm_backward(dy, h, w, r, dres=dres)
+    ws = torch.empty(fb.fp8_rmsnorm_backward_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+    dx, dw2 = dy if over == "dy" else dres, torch.empty_like(dw)
+    fb.fp8_rmsnorm_backward(dy, h, w, r, ws, dx, dw2, dres=dres)
+    assert torch.equal(dx, want) and torch.equal(dw, dw2)
+
+
 def test_rows_beyond_32_bit_offsets():
     rows, cols = 262144 + 3, 16384
     x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")

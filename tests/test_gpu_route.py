@@ -120,6 +120,32 @@ def test_keys_closer_than_fp32_tells_apart(score, gs):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("base", [0.5, -0.5, 100.0, -1000.0])
+@pytest.mark.parametrize("experts,groups,tokens", [(64, 4, 5), (256, 8, 5), (1024, 16, 3), (256, 8, 4100), (96, 3, 40)])
+def test_keys_a_few_steps_apart(score, base, experts, groups, tokens):
+    """Equal scores and biases one to some fp32 steps apart: the key's own low bits decide."""
+    rng = np.random.default_rng(experts + tokens)
+    l64 = np.full((tokens, experts), 0.25)
+    l = torch.from_numpy(l64.astype(np.float32)).cuda()
+    step = float(np.spacing(np.float32(abs(base))))
+    bias = base + step * rng.permutation(experts)
+    _check(l, l64, bias, 8, score)
+    _check(l, l64, bias, 8, score, groups, 2, "top2")
+    _check(l, l64, bias, 8, score, groups, 1, "max", renorm=True)
+
+
+def test_bias_that_is_not_aligned_for_four():
+    rng = np.random.default_rng(33)
+    for experts, tokens in ((256, 3), (256, 4200), (64, 50)):
+        l, _ = _logits(rng, tokens, experts, torch.float32)
+        bias = torch.randn(experts + 1, device="cuda")[1:]
+        assert bias.data_ptr() % 16
+        got = fb.moe_route(l, 6, bias=bias, score="sigmoid", groups=8, topk_groups=3, group_score="top2")
+        want = fb.moe_route(l, 6, bias=bias.clone(), score="sigmoid", groups=8, topk_groups=3, group_score="top2")
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_group_sums_that_cancel(score):
     """Two best keys of a group that are large and of opposite sign: their sum is small, its rounding is not."""
     rng = np.random.default_rng(31)
