@@ -15,8 +15,8 @@ namespace {
 // Threads of a workgroup at most.  Forward, one chunk each: 16384 tokens of
 // eight rows of 7168 take 412 us (5.7 TB/s) with 128; an earlier form of the
 // kernel 470 with 128, 474 with 64, 493 with 192 and 500 to 520 with 256 to
-// 896.  Backward, a whole token: 4093 such tokens take 203 us (4.9 TB/s) with
-// 512; the earlier form 206, 207 with 256, 212 with 128.
+// 896.  Backward, a whole token: 4093 such tokens take 201 us (4.95 TB/s)
+// with 512, 200 with 256 and with 1024.
 constexpr int kCbThreads = 128;
 constexpr int kCbBwdThreads = 512;
 
