@@ -250,7 +250,9 @@ __device__ __forceinline__ void mfma_rows(const MatvecArgs& a, int grp, int lo, 
   const Buffer xb = make_buffer(a.x, (uint32_t)(a.x_rows * K * 2));
   uint8_t* lds = smem + wave * S::kBytes;
 
-  for (int m0 = lo; m0 < hi; m0 += MX) {
+  // unsigned: hi can lie within MX of 2^31
+  for (uint32_t next = (uint32_t)lo; next < (uint32_t)hi; next += MX) {
+    const int m0 = (int)next;
     const int mr = hi - m0 < MX ? hi - m0 : MX;
     uint32_t x0[XI];
 #pragma unroll

@@ -235,3 +235,24 @@ def test_a_large_matrix_is_its_rows(m):
     for j in range(0, n, 10000):
         one = fb.nvfp4_matvec(x, q[j:j + 10000], bs[j:j + 10000], gs, out_dtype=torch.float32)
         assert torch.equal(y[:, j:j + 10000], one)
+
+
+@pytest.mark.parametrize("k", [64, 48])
+def test_rows_up_to_the_largest_count(k):
+    """The last rows of the largest call, more of them than one pass takes: the pass after the last one would begin
+    past 2^31.  Rows before the group are left as they were."""
+    print(f"[grouped matvec] rows up to 2^31 - 2, k {k}", flush=True)
+    total, rows = (1 << 31) - 1, 37
+    rng = np.random.default_rng(k)
+    x = rng.integers(-8, 9, (5, k)).astype(np.float64)
+    q, bs = _grid_matrix(rng, 1, k)
+    ri = torch.zeros(total, dtype=torch.int32, device="cuda")
+    tail = rng.integers(0, 5, rows)
+    ri[-rows:] = torch.from_numpy(tail.astype(np.int32)).cuda()
+    off = torch.tensor([total - rows, total], dtype=torch.int32, device="cuda")
+    y = torch.full((total, 1), 9.0, dtype=torch.bfloat16, device="cuda")
+    fb.fp8_nvfp4_grouped_matvec(bf16_from_bits(f32_to_bf16(x.astype(np.float32))), ri, torch.from_numpy(q[None]).cuda(),
+                                torch.from_numpy(bs[None]).cuda(), torch.ones(1, device="cuda"), 1, off, y)
+    want = x[tail] @ moe.nvfp4_matrix(q, bs, [1.0], 1).T
+    assert np.array_equal(_out(y[-rows:]), _bf16(want))
+    assert torch.all(y[:-rows] == 9.0)
