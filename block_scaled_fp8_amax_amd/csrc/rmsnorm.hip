@@ -137,17 +137,20 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormParams p) {
   ss = block_sum(ss, red[turn][0]);
   float rstd = 1.0f / sqrtf(ss / p.cols + p.eps);
   if (!(ss < __builtin_inff())) {
-    // squares left the fp32 range: the same with h 2^-64 (uniform branch)
+    // squares left the fp32 range: the same with h 2^-96 (uniform branch).
+    // The largest row, 32768 elements below 2^128, sums up to less than 2^79
+    // so, and a sum of squares of 2^128 to 2^-64.  eps takes the factor
+    // 2^-192 in two steps.
     float s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = f[i][j] * 0x1p-64f;
+        const float d = f[i][j] * 0x1p-96f;
         s2 = __builtin_fmaf(d, d, s2);
       }
     s2 = block_sum(s2, red[turn][1]);
-    rstd = 0x1p-64f / sqrtf(s2 / p.cols + p.eps * 0x1p-128f);
+    rstd = 0x1p-96f / sqrtf(s2 / p.cols + p.eps * 0x1p-96f * 0x1p-96f);
   }
   if (p.rstd && t == 0) p.rstd[row] = rstd;
 

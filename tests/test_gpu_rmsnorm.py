@@ -297,3 +297,56 @@ def test_backward_against_differences_of_the_kernel():
     tol = 2.0 ** -8 * (np.abs(dy) * (np.abs(ys[0]) + np.abs(ys[1]))).sum() + curve
     dxf = _f64(bf16_bits(dx))
     assert abs(got - (dxf * moved).sum()) <= tol + 2.0 ** -8 * np.abs(dxf * moved).sum()
+
+
+# The largest rows: rstd is below the normal range there, where its own rounding is half a step of 2^-149, at most
+# 2^-22 of 1 / 2^128, within the 2^-18 that rstd is checked to and the D of y.
+@pytest.mark.parametrize("block", ["1x128", "1x32"])
+@pytest.mark.parametrize("cols", [128, 1152, 7168, 32768])
+@pytest.mark.parametrize("size", [1e36, 1e37, 1e38, 3.38e38])
+def test_forward_of_rows_up_to_the_largest_value(size, cols, block):
+    print(f"[rmsnorm] rows of {size}, {cols} columns, {block}", flush=True)
+    rng = np.random.default_rng(cols)
+    x = rng.uniform(0.5, 1, (4, cols)) * size * rng.choice([-1, 1], (4, cols))
+    x[0] = size                                  # no smaller element
+    x[1, 1:] *= 1e-30                            # one large element among small ones
+    _check(_bits(x), None, torch.float32, block, "ceil", 21)
+    half = _bits(x / 2)
+    _check(half, half, torch.bfloat16, block, "ceil", 22)
+
+
+@pytest.mark.parametrize("cols", [32, 96])
+@pytest.mark.parametrize("size", [1e36, 7e37, 3.38e38])
+def test_forward_of_narrow_rows_up_to_the_largest_value(size, cols):
+    x = np.full((3, cols), size) * np.random.default_rng(cols).choice([-1, 1], (3, cols))
+    _check(_bits(x), None, torch.float32, "1x32", "floor", 23)
+
+
+@pytest.mark.parametrize("cols", [128, 7168])
+def test_forward_where_the_sum_of_squares_leaves_the_fp32_range(cols):
+    """Rows whose sum of squares is just below and just above 2^128, with an eps that does not count and ones that
+    do."""
+    edge = 2.0 ** 64 / np.sqrt(cols)
+    x = np.stack([np.full(cols, f * edge) for f in (0.5, 0.98, 0.995, 1.0, 1.005, 1.02, 1.5, 2.0)])
+    for eps in (1e-6, 1e30, 1e38):
+        _check(_bits(x), None, torch.float32, "1x128", "ceil", 24, eps=eps)
+
+
+@pytest.mark.parametrize("rows,cols", [(5, 128), (300, 7168), (3, 32768)])
+@pytest.mark.parametrize("size", [1e37, 3.38e38])
+def test_backward_of_rows_up_to_the_largest_value(size, rows, cols):
+    """With the rstd of the forward call, which is below the normal range."""
+    rng = np.random.default_rng(rows)
+    hb = _bits(rng.uniform(0.5, 1, (rows, cols)) * size * rng.choice([-1, 1], (rows, cols)))
+    dyb = _bits(1e30 * rng.standard_normal((rows, cols)))
+    w, w64 = _weight(rng, cols, torch.float32)
+    h, dy = bf16_from_bits(hb), bf16_from_bits(dyb)
+    rstd = fb.rmsnorm_quantize(h, w, EPS, save_rstd=True)["rstd"]
+    dx, dw = fb.rmsnorm_backward(dy, h, w, rstd)
+    dy64, h64, r64 = _f64(dyb), _f64(hb), rstd.double().cpu().numpy()
+    assert np.all(np.abs(r64 * np.sqrt((h64 ** 2).mean(1)) - 1) <= 2.0 ** -18)
+    want, wantw = moe.rmsnorm_backward(dy64, h64, w64, r64)
+    xh, wd = np.abs(h64 * r64[:, None]), np.abs(dy64 * w64)
+    mag = r64[:, None] * (wd + xh * (wd * xh).mean(1)[:, None])
+    assert np.all(np.abs(_f64(bf16_bits(dx)) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -17 * mag), "dx"
+    assert np.all(np.abs(dw.double().cpu().numpy() - wantw) <= 2.0 ** -16 * (np.abs(dy64) * xh).sum(0)), "dw"
