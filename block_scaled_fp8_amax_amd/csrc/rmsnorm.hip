@@ -135,9 +135,11 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormParams p) {
     for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(f[i][j], f[i][j], ss);
   }
   ss = block_sum(ss, red[turn][0]);
-  float rstd = 1.0f / sqrtf(ss / p.cols + p.eps);
-  if (!(ss < __builtin_inff())) {
-    // squares left the fp32 range: the same with h 2^-96 (uniform branch).
+  const float mean = ss / p.cols + p.eps;
+  float rstd = 1.0f / sqrtf(mean);
+  if (!(mean < __builtin_inff())) {
+    // squares (or their mean and eps) left the fp32 range: the same with h
+    // 2^-96 (uniform branch).
     // The largest row, 32768 elements below 2^128, sums up to less than 2^79
     // so, and a sum of squares of 2^128 to 2^-64.  eps takes the factor
     // 2^-192 in two steps.

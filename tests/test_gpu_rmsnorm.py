@@ -350,3 +350,15 @@ def test_backward_of_rows_up_to_the_largest_value(size, rows, cols):
     mag = r64[:, None] * (wd + xh * (wd * xh).mean(1)[:, None])
     assert np.all(np.abs(_f64(bf16_bits(dx)) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -17 * mag), "dx"
     assert np.all(np.abs(dw.double().cpu().numpy() - wantw) <= 2.0 ** -16 * (np.abs(dy64) * xh).sum(0)), "dw"
+
+
+@pytest.mark.parametrize("cols", [128, 7168])
+def test_forward_where_the_mean_and_eps_leave_the_fp32_range(cols):
+    """Their sum can where the sum of squares does not: eps is any finite value."""
+    rng = np.random.default_rng(25)
+    sign, top = rng.choice([-1, 1], (4, cols)), 0.999 * 2.0 ** 64 / np.sqrt(cols)
+    rows = [_bits(top * sign), _bits(1.001 * top * sign), _bits(1e15 * rng.standard_normal((4, cols))),
+            _bits(3e38 * sign)]
+    for eps in (3.3e38, 3.4028234e38):
+        for x in rows:
+            _check(x, None, torch.float32, "1x128", "ceil", 27, eps=eps)
