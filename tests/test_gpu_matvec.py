@@ -256,3 +256,82 @@ def test_rows_up_to_the_largest_count(k):
     want = x[tail] @ moe.nvfp4_matrix(q, bs, [1.0], 1).T
     assert np.array_equal(_out(y[-rows:]), _bf16(want))
     assert torch.all(y[:-rows] == 9.0)
+
+
+# Both ways to multiply (dot products for one or two rows on large grids, the matrix cores otherwise) on values of
+# the whole range.  An e2m1 code times the power of two of its scale is exact, and so is its product with x; the
+# scale's mantissa, the additions, the tensor scale and fp32 results below the normal range (half of 2^-149 for
+# each of the K / 16 blocks' sums and K products) round.
+def _range_check(x, q, bs, gs, y, what, nan_rows=()):
+    w = moe.nvfp4_matrix(q, bs, gs, len(q))
+    ok = np.ones(len(q), bool)
+    ok[list(nan_rows)] = False
+    want, mag = x @ w[ok].T, np.abs(x) @ np.abs(w[ok]).T
+    assert mag.max() < 3.4e38, "the case itself leaves the fp32 range"
+    k = x.shape[1]
+    got = _out(y)
+    tol = (k + k // 16) * 2.0 ** -24 * mag + 2.0 ** -23 * np.abs(want) + 2 * k * 2.0 ** -149 * float(gs[0])
+    bad = np.argwhere(~(np.abs(got[:, ok] - want) <= tol + 2.0 ** -149))
+    assert len(bad) == 0, (what, len(bad), bad[0], got[:, ok][tuple(bad[0])], want[tuple(bad[0])])
+    assert np.all(np.isnan(got[:, ~ok])), what
+
+
+def _range_case(rng, kind, m, n, k):
+    """x [m, k] as bf16 bits, codes and scale bytes of every value but NaN, but as large x allows."""
+    q = rng.integers(0, 256, (n, k // 2)).astype(np.uint8)
+    bs = rng.integers(0, 256, (n, k // 16)).astype(np.uint8)
+    bs[(bs & 0x7F) == 0x7F] = 0x80                       # zeros, of either sign, among them
+    bs[rng.random(bs.shape) < 0.1] = 0
+    x = rng.standard_normal((m, k))
+    if kind == "large":                                  # a few elements near the largest value, under small scales
+        at = rng.permutation(k // 16)[:2] * 16 + rng.integers(0, 16, 2)
+        x[:, at] = rng.choice([-1, 1], (m, 2)) * np.array([3.3e38, 2e37])
+        small = rng.integers(0, 0x11, (n, 2)) | rng.choice([0, 0x80], (n, 2))       # up to 2^-5
+        small[rng.random(small.shape) < 0.3] = 0
+        bs[:, at // 16] = small
+    elif kind == "small":
+        x *= 2.0 ** -124
+    return f32_to_bf16(x.astype(np.float32)), q, bs
+
+
+@pytest.mark.parametrize("kind", ["usual", "large", "small"])
+@pytest.mark.parametrize("m", [1, 2, 3, 20])
+@pytest.mark.parametrize("n,k", [(16400, 192), (16416, 1088), (300, 2064)])
+def test_values_of_the_whole_range(kind, m, n, k):
+    print(f"[matvec] {kind} values, {m}x{n}x{k}", flush=True)
+    rng = np.random.default_rng(m + n)
+    xb, q, bs = _range_case(rng, kind, m, n, k)
+    gs = np.array([0.37], np.float32)
+    y = fb.nvfp4_matvec(bf16_from_bits(xb), torch.from_numpy(q).cuda(), torch.from_numpy(bs).cuda(),
+                        torch.from_numpy(gs).cuda(), out_dtype=torch.float32)
+    _range_check(bf16_to_f32(xb).astype(np.float64), q, bs, gs, y, kind)
+
+
+@pytest.mark.parametrize("kind", ["usual", "large", "small"])
+def test_grouped_values_of_the_whole_range(kind):
+    """Groups of up to two rows and larger ones in one call of a large grid."""
+    sizes, n, k = [1, 2, 0, 1, 5, 1, 1, 0, 2, 1, 2, 1, 2, 1, 0, 2] * 2, 600, 320
+    rng = np.random.default_rng(12)
+    case = [_range_case(rng, kind, s, n, k) for s in sizes]
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    gs = np.full(len(sizes), 0.37, np.float32)
+    y = fb.nvfp4_grouped_matvec(bf16_from_bits(np.concatenate([c[0] for c in case])),
+                                torch.from_numpy(np.stack([c[1] for c in case])).cuda(),
+                                torch.from_numpy(np.stack([c[2] for c in case])).cuda(), torch.from_numpy(gs).cuda(),
+                                torch.from_numpy(off).cuda(), out_dtype=torch.float32)
+    for g, (xb, q, bs) in enumerate(case):
+        if sizes[g]:
+            _range_check(bf16_to_f32(xb).astype(np.float64), q, bs, gs[:1], y[off[g]:off[g + 1]], (kind, g))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 16400, 192), (2, 16400, 192), (5, 16400, 192), (1, 40, 192), (3, 40, 208)])
+def test_a_scale_byte_that_is_nan(m, n, k):
+    """Its products are NaN, whatever the codes and x; the other matrix rows are as they would be."""
+    rng = np.random.default_rng(m + n)
+    xb, q, bs = _range_case(rng, "usual", m, n, k)
+    q[[3, n - 1]] = 0                                    # codes of 0
+    bs[3, 0], bs[17, k // 16 - 1], bs[n - 1, 5] = 0x7F, 0xFF, 0x7F
+    gs = np.ones(1, np.float32)
+    y = fb.nvfp4_matvec(bf16_from_bits(xb), torch.from_numpy(q).cuda(), torch.from_numpy(bs).cuda(),
+                        torch.from_numpy(gs).cuda(), out_dtype=torch.float32)
+    _range_check(bf16_to_f32(xb).astype(np.float64), q, bs, gs, y, "NaN scale", nan_rows=(3, 17, n - 1))
