@@ -123,9 +123,11 @@ __global__ __launch_bounds__(kCbBwdThreads) void combine_bwd_kernel(CombineBwdAr
     for (int j0 = 0; j0 < a.top_k; j0 += KB, turn ^= 1) {
       Buffer rb[KB], db[KB];
       float w[KB], dot[KB];
+      int in = 0;                                      // bit j: choice j takes part
 #pragma unroll
       for (int j = 0; j < KB; ++j) {
         const int64_t s = j0 + j < a.top_k ? a.slot[tok * a.top_k + j0 + j] : -1;
+        in |= (s >= 0 && s < a.total_m ? 1 : 0) << j;
         w[j] = s >= 0 && s < a.total_m ? a.weights[tok * a.top_k + j0 + j] : 0.f;
         rb[j] = row_buffer<ROW_F32>(a.rows, s, a.total_m, a.n);
         db[j] = row_buffer<ROW_F32>(a.drows, s, a.total_m, a.n);
@@ -162,7 +164,8 @@ __global__ __launch_bounds__(kCbBwdThreads) void combine_bwd_kernel(CombineBwdAr
       if (t < KB && j0 + t < a.top_k) {
         float s = 0.f;
         for (int v = 0; v < threads / 64; ++v) s += red[turn][v][t];
-        a.dweights[tok * a.top_k + j0 + t] = s;
+        // a pair left out gets 0 whatever dy holds
+        a.dweights[tok * a.top_k + j0 + t] = (in >> t) & 1 ? s : 0.f;
       }
     }
   }

@@ -235,7 +235,8 @@ int fp8_moe_combine(const void* rows, int row_type, int64_t total_m, const int32
  * (the residual's gradient is dy itself).  drows is of row_type, rounded
  * once; rows that no slot names are left as they were.  Slots are distinct,
  * as fp8_moe_plan's are; a row that two slots name ends with elements of
- * either gradient.  A slot outside [0, total_m) gets dweight 0.
+ * either gradient.  A slot outside [0, total_m) gets dweight 0, whatever dy
+ * holds.
  *
  * dy [tokens x n] bf16 or float per dy_type; other arguments as above.
  */

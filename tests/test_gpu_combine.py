@@ -169,3 +169,30 @@ def test_backward_against_differences():
         want = (_np(moved) * _np(grad)).sum()
         mag = (np.abs(_np(dy)) * (np.abs(up) + np.abs(dn))).sum() + (np.abs(_np(moved) * _np(grad))).sum()
         assert abs(got - want) <= 64 * 2.0 ** -24 * mag
+
+
+@pytest.mark.parametrize("row_dtype", [BF, F32])
+@pytest.mark.parametrize("dy_dtype", [BF, F32])
+@pytest.mark.parametrize("top_k", [1, 2, 3, 8, 11])
+def test_backward_of_left_out_pairs_whatever_dy_holds(top_k, dy_dtype, row_dtype):
+    """A slot outside the rows gets a weight gradient of 0 where dy is infinite or NaN too; finite tokens beside such
+    ones keep theirs."""
+    rng = np.random.default_rng(top_k)
+    tokens, n, total = 5, 264, 5 * top_k
+    rows, dy = _t(rng.standard_normal((total, n)), row_dtype), _t(rng.standard_normal((tokens, n)), dy_dtype)
+    clean = dy.clone()
+    dy[1] = float("inf")
+    dy[2, 7], dy[2, 260] = float("nan"), -float("inf")
+    dy[4] = float("nan")
+    slot = _slots(rng, tokens, top_k, total)
+    slot[rng.random(slot.shape) < 0.4] = -1
+    slot[1, 0], slot[2, top_k - 1] = total, -5
+    slot[4] = np.where(np.arange(top_k) % 2, np.iinfo(np.int32).max, np.iinfo(np.int32).min)
+    st, w = torch.from_numpy(slot).cuda(), _t(rng.uniform(-1, 1, (tokens, top_k)), F32)
+    dw = torch.full((tokens, top_k), 9.0, dtype=F32, device="cuda")
+    fb.fp8_moe_combine_backward(dy, rows, st, w, torch.empty_like(rows), dw)
+    want = fb.moe_combine_backward(clean, rows, st, w)[1]
+    out = torch.from_numpy((slot < 0) | (slot >= total)).cuda()
+    assert torch.all(dw[out] == 0)
+    assert torch.equal(dw[[0, 3]], want[[0, 3]])
+    assert not torch.any(torch.isfinite(dw[[1, 2]]) & ~out[[1, 2]])
