@@ -340,3 +340,65 @@ def test_plan_workspace_holds_garbage():
     fb.fp8_moe_plan(torch.from_numpy(ids).cuda(), 64, ws, off, row, slot)
     for got, ref in zip((off, row, slot), moe.plan(ids, 64)):
         assert np.array_equal(got.cpu().numpy(), ref)
+
+
+def _sampled_check(l, rows, bias, top_k, score, groups, kept, gs, renorm):
+    """A call over all tokens against the oracle on the tokens ``rows``."""
+    l64 = l[rows].double().cpu().numpy()
+    ids, w = fb.moe_route(l, top_k, bias=None if bias is None else torch.from_numpy(bias.astype(np.float32)).cuda(),
+                          score=score, groups=groups, topk_groups=kept, group_score=gs, renorm=renorm)
+    want, ww = moe.route(l64, None if bias is None else bias.astype(np.float32), top_k, score, groups, kept, gs,
+                         renorm)
+    ids, w = ids[rows].cpu().numpy(), w[rows].cpu().numpy()
+    bad = np.argwhere(ids != want)
+    assert len(bad) == 0, (len(bad), rows[bad[0][0]], ids[bad[0][0]], want[bad[0][0]])
+    tol = 2.0 ** -18 + 2.0 ** -22 * _spread(l64)
+    assert np.all(np.abs(w - ww) <= tol * np.abs(ww) + 2.0 ** -126), np.abs(w - ww).max()
+
+
+@pytest.mark.parametrize("tokens,experts,groups,kept,top_k", [
+    # 16 lanes to a token: groups of two lanes, of one, and of parts of lanes
+    (4101, 128, 8, 3, 8), (4101, 96, 12, 5, 6), (4101, 120, 8, 3, 7), (4101, 112, 16, 6, 20), (4101, 68, 4, 2, 5),
+    # 32 lanes, many tokens
+    (4101, 256, 8, 4, 8), (4101, 160, 8, 3, 6), (4101, 192, 24, 7, 4),
+    # 64 lanes, eight experts each: whole lanes and parts of them
+    (37, 512, 8, 3, 8), (37, 384, 8, 3, 8), (37, 320, 10, 4, 9), (37, 512, 64, 9, 40), (37, 260, 13, 2, 11),
+    # 64 lanes, sixteen experts each
+    (37, 768, 3, 2, 8), (37, 1000, 8, 3, 64), (37, 600, 12, 5, 6), (37, 1024, 32, 4, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("gs", ["max", "top2"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_groups_of_every_launch_shape(tokens, experts, groups, kept, top_k, score, gs, biased):
+    print(f"[route] {tokens}x{experts}, {kept} of {groups} groups, top {top_k} {score} {gs} bias={biased}", flush=True)
+    rng = np.random.default_rng(tokens + experts + groups)
+    l = 1.5 * rng.standard_normal((tokens, experts)).astype(np.float32)
+    l[::3] = np.round(l[::3] * 2) / 2                     # ties, of experts and of groups
+    l[1::7][rng.random(l[1::7].shape) < 0.6] = -np.inf
+    per = experts // groups
+    l[2::9, :per] = -np.inf                               # a group of none
+    l[5] = -np.inf
+    l[tokens - 1, 1:] = -np.inf
+    near = np.float32(0.7) + rng.integers(-40, 41, experts).astype(np.float32) * np.float32(2.0 ** -24)
+    l[4] = l[tokens - 3] = near                           # scores closer than fp32 tells apart
+    bias = 0.1 * rng.standard_normal(experts)
+    bias[rng.integers(0, experts, 3)] = -np.inf
+    rows = list(range(37)) + ([] if tokens == 37 else list(range(tokens - 40, tokens)))
+    _sampled_check(torch.from_numpy(l).cuda(), rows, bias if biased else None, top_k, score, groups, kept, gs,
+                   renorm=experts % 3 == 0)
+    if biased:
+        flat = np.where(rng.random(experts) < 0.5, 8.0, 8.0 + 2.0 ** -20)      # hides the scores' low bits
+        _sampled_check(torch.from_numpy(l).cuda(), rows, flat, top_k, score, groups, kept, gs, renorm=True)
+
+
+@pytest.mark.parametrize("tokens,experts,top_k", [(4101, 128, 8), (4101, 70, 20), (4101, 255, 8), (37, 512, 8),
+                                                  (37, 300, 64), (37, 777, 12)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_no_groups_in_every_launch_shape(tokens, experts, top_k, score, biased):
+    rng = np.random.default_rng(tokens + experts)
+    l = 1.5 * rng.standard_normal((tokens, experts)).astype(np.float32)
+    l[::3] = np.round(l[::3] * 2) / 2
+    l[1::7][rng.random(l[1::7].shape) < 0.6] = -np.inf
+    bias = 0.1 * rng.standard_normal(experts)
+    rows = list(range(37)) + ([] if tokens == 37 else list(range(tokens - 40, tokens)))
+    _sampled_check(torch.from_numpy(l).cuda(), rows, bias if biased else None, top_k, score, 1, 1, "max", True)
