@@ -362,3 +362,44 @@ def test_forward_where_the_mean_and_eps_leave_the_fp32_range(cols):
     for eps in (3.3e38, 3.4028234e38):
         for x in rows:
             _check(x, None, torch.float32, "1x128", "ceil", 27, eps=eps)
+
+
+@pytest.mark.parametrize("wdtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("block,rule", [("1x128", "ceil"), ("1x32", "ceil"), ("1x32", "floor")])
+def test_forward_of_values_below_the_normal_range(block, rule, wdtype):
+    """Tiles of y from 1e-35 down to zeros: fp32 scales with few bits or none, E8M0 scales at their least.  y itself
+    is rounded to a multiple of 2^-149 there, at most half of that off besides D, and so is an fp32 scale; a code
+    lies between those of the quotients at both ends of y, by the scale that was stored, and has y's sign.  Where
+    that scale is 0 the code is 0."""
+    rng = np.random.default_rng(31)
+    rows, cols, n = 7, 2048, 32 if block == "1x32" else 128
+    xb = _values(rng, rows, cols, "normal")
+    size = np.repeat(10.0 ** -np.arange(35, 35 + cols // 128, dtype=np.float64), 128)
+    w = torch.from_numpy((size * rng.uniform(0.5, 1, cols) * rng.choice([-1, 1], cols)).astype(np.float32)).to(wdtype)
+    w64 = w.double().numpy()
+    q, scale, _, yb, ydq, rstd = _run(xb, None, w.cuda(), block, rule)
+    y, r = moe.rmsnorm(_f64(xb), w64, EPS)
+    half = 2.0 ** -150
+    assert np.all(np.abs(rstd - r) <= 2.0 ** -18 * r)
+    assert np.all(np.abs(_f64(yb) - y) <= (2.0 ** -8 + D) * np.abs(y) + half + 2.0 ** -134), "y"
+    amax = np.abs(y).reshape(rows, cols // n, n).max(-1)
+    if block == "1x32":
+        lo, hi = (quant.e8m0_exponent(amax * (1 + s * D) + s * half, rule) for s in (-1, 1))
+        X = scale.astype(np.int64) - 127
+        assert np.all((X == lo) | (X == hi)) and np.any(X == -127)
+        sv = np.exp2(X.astype(np.float64))
+    else:
+        assert np.all(np.abs(scale - amax / 448) <= (2 * D * amax + half) / 448 + half), "fp32 scale"
+        assert np.any(scale == 0) and np.any((scale > 0) & (scale < 2.0 ** -126))
+        sv = scale.astype(np.float64)
+    per = np.repeat(sv, n, axis=1)
+    mag, got = np.abs(y), np.abs(e4m3_decode(q).astype(np.float64))
+    zero = per == 0
+    by = np.where(zero, 1.0, per)
+    least = e4m3_decode(e4m3_encode(np.maximum(mag * (1 - D) - half, 0) / by))
+    most = e4m3_decode(e4m3_encode((mag * (1 + D) + half) / by))
+    bad = np.argwhere(~zero & ((got < least) | (got > most)))
+    assert len(bad) == 0, (len(bad), bad[0], q[tuple(bad[0])], y[tuple(bad[0])], per[tuple(bad[0])])
+    assert np.all(got[zero] == 0)
+    assert np.array_equal(q >= 0x80, np.signbit(y)), "signs"
+    assert_bytes_equal(ydq, quant.dequantize(q, scale, block), "ydq")
