@@ -77,11 +77,12 @@ constexpr int64_t kMaxGrid = int64_t(1) << 20;
 // Bytes of a call past which its accesses are nontemporal: what it reads and
 // writes does not stay in the 256 MB of the Infinity Cache anyway, and that
 // way its stores and loads disturb each other less.  16384 x 8 rows of 7168
-// combined: 412 us, 457 with the cache's own policy; norm of 16384 x 7168: 183
-// and 186, its gradient for 8192 x 7168: 91 and 96; NVFP4 weights of 52 experts
-// of 4096 x 7168: 153 and 163.  Smaller calls find their inputs in the cache
-// and leave their outputs there (2048 x 7168 normed, 132 MB: 23.9 us,
-// nontemporal 27.3; weights of 8 such experts: 30 and 33).
+// combined: 416 us, 460 with the cache's own policy; norm of 16384 x 7168: 180
+// and 188, its gradient for 8192 x 7168: 90 and 96; NVFP4 weights of 52 experts
+// of 4096 x 7168: 149 and 164.  Smaller calls find their inputs in the cache
+// and leave their outputs there (2048 x 7168 normed, 132 MB: 23.0 us,
+// nontemporal 27.9; weights of 8 such experts, two sets in turn: 25.8 and
+// 27.4).
 constexpr int64_t kCached = int64_t(256) << 20;
 
 struct RmsNorm {

@@ -16,7 +16,7 @@
 //     row, v_dot2_f32_bf16 on the unscaled values of a block and one fused
 //     multiply by its scale: 1.7 instructions per weight at two rows, no
 //     LDS.  Taken for groups of at most two rows on large grids: 64 rows on
-//     52 experts of 4096 x 7168 in 153 us (5.6 TB/s), against 185 us on the
+//     52 experts of 4096 x 7168 in 150 us (5.7 TB/s), against 185 us on the
 //     matrix cores; on grids of up to 256 tiles it was 7% slower at two rows.
 #include "device.h"
 #include "launch.h"

@@ -12,7 +12,7 @@
 // of the row in registers between the sum of squares and the encode, so the
 // row is read once; a 1x128 tile is 16 adjacent lanes, a 1x32 block 4.  Bound
 // by HBM for many rows: 16384 x 7168 with residual, h and y, 9 bytes per
-// element, in 183 us (5.8 TB/s).  A few rows are bound by latency: 3.9 us.
+// element, in 180 us (5.9 TB/s).  A few rows are bound by latency: 3.9 us.
 #include "device.h"
 #include "launch.h"
 
@@ -235,8 +235,9 @@ struct NormBwdParams {
 
 // Workgroup b takes the rows b, b + G, ...; the weight gradient of its rows
 // stays in registers and goes to the workspace once.  Bound by reading dy, h
-// and dres and writing dx: 8192 x 7168 in 89 us with the partials' sum (5.3
-// TB/s).  Rows wider than 16384 are read twice (the second time from the L2):
+// and dres and writing dx: 8192 x 7168 in 90 us with the partials' sum (5.2
+// TB/s).  A few thousand small rows are bound by the two dependent launches and
+// the partials' way through memory (2352 x 512: 8.7 us, its bytes 2).  Rows wider than 16384 are read twice (the second time from the L2):
 // kept in registers they spill, 2048 x 32768 in 233 us instead of 161.  Two
 // rows at a time, rows kept packed across the barrier and dres
 // loaded before it all took registers that cost a workgroup per CU, and 10 to
@@ -355,8 +356,10 @@ __global__ __launch_bounds__(512) void rmsnorm_dw_kernel(const v4f* __restrict__
 }
 
 // Chunks per thread and threads for a row of nch chunks: two chunks where
-// there are rows enough to fill the card (16384 x 7168 forward: 186 us
-// against 196 with one), one for a few rows (one row: 4.0 us against 4.3).
+// there are rows enough to fill the card (7168 columns forward, 16384 rows: 180
+// us against 184 with one, 2048: 23 against 28, 768: 11.5 against 12.7, from
+// 384 to 512 the same), one for a few rows (2048 columns, one row: 3.2 us
+// against 3.7, 511: 4.6 against 5.2, 1024: the same).
 void row_shape(int nch, int64_t rows, int* ch, int* threads) {
   *ch = nch <= 1024 && (rows < 512 || nch <= 128) ? 1 : nch <= 2048 ? 2 : 4;
   *threads = ((nch + *ch - 1) / *ch + 63) / 64 * 64;
@@ -364,11 +367,11 @@ void row_shape(int nch, int64_t rows, int* ch, int* threads) {
 
 // Workgroups of the backward pass: 16 waves per CU, four workgroups at most,
 // and two where one has more than eight waves, so that one's loads run beside
-// the other's barrier (8192 x 7168: 84 us, 94 with one, 100 with four; 8192 x
-// 512: 13 us with four, 21 with sixteen).  A workgroup takes two rows and,
-// past 256 workgroups, four, so that the partial sums stay a small part of
-// the traffic (500 x 7168: 15 us, 21 with one row each; 2352 x 512: 9 us, 14
-// with one).
+// the other's barrier (8192 x 7168: 90 us, 106 with one, 108 with four; 8192 x
+// 512: 14 us with four, 29 with one, 19 with two, 14 with sixteen).  A
+// workgroup takes two rows and, past 256 workgroups, four, so that the partial
+// sums stay a small part of the traffic (500 x 7168: 12.7 us, 15.6 with one
+// row each; 2352 x 512: 8.7 us, 9.0 with one).
 int64_t bwd_parts(int64_t rows, int threads, int ch) {
   const int waves = threads / 64, least = ch == 1 ? 2 : 1;
   int per_cu = 16 / waves > least ? 16 / waves : least;

@@ -712,7 +712,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a, int vec,
 // by itself (64 runs of 256 experts: fewer launches and 64 loads per
 // thread); for more, plan_scan_kernel turns the counts into running sums
 // first.  A single run counts and places in one launch.  Bound by latency and
-// LDS: 131072 pairs of 256 experts, count 4.7 us and place 6.9 us.
+// LDS: 131072 pairs of 256 experts, count 3.9 us and place 7.9 us.
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanItems = 4;                              // pairs per lane

@@ -53,7 +53,8 @@ typedef enum { FP8_GROUP_MAX = 0, FP8_GROUP_TOP2 = 1 } fp8_group_score;
  * code = e4m3(y / scale)) or 1x32 blocks (E8M0 exponent X by `rule`, code =
  * e4m3(y * 2^-X)) as fp8_block_quantize does, but from the fp32 y.  A tile
  * whose fp32 scale is 0 gets codes +-0.  Rows whose h or y leaves its range
- * (bf16, fp32) have no defined codes.
+ * (bf16, fp32) have no defined codes; a NaN in a row shows in its y and rstd,
+ * not in its codes.
  *
  * x        [rows x cols] bf16 (16-byte aligned);
  * residual optional (NULL = none) [rows x cols] bf16 (16-byte aligned);
@@ -86,6 +87,9 @@ int fp8_rmsnorm_quantize(const uint16_t* x, const uint16_t* residual, const void
  *                                            residual alike)
  *   dweight = sum over rows of dy xh
  * dres is the gradient that reaches h past the norm (the residual stream).
+ * Sums are fp32: a row of which the |weight dy| or the |weight dy xh| add up
+ * past that range has no defined dx, a column of which the |dy xh| do no
+ * defined dweight.
  *
  * dy     [rows x cols] bf16 (16-byte aligned); h [rows x cols] bf16, the h
  *        of the forward call (x where it had no residual); weight as there;
@@ -114,7 +118,9 @@ int fp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes);
  *     renorm, times `scale`
  * Ties go to the lowest index, of groups and of experts.  Choices are those
  * of the scores in double precision (without a bias: of the logits
- * themselves), whatever the precision of the weights.
+ * themselves); weights are computed in fp32, off by at most 2^-18 + 2^-22 L
+ * of their value, L the largest difference of two finite logits of the token
+ * (about 2^-24 for usual logits).
  *
  * logits [tokens x experts] bf16 or float per logits_type (4-byte aligned,
  *        bf16 2-byte).  An expert whose logit is -inf or NaN is masked: its
