@@ -139,10 +139,9 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormParams p) {
   float rstd = 1.0f / sqrtf(mean);
   if (!(mean < __builtin_inff())) {
     // squares (or their mean and eps) left the fp32 range: the same with h
-    // 2^-96 (uniform branch).
-    // The largest row, 32768 elements below 2^128, sums up to less than 2^79
-    // so, and a sum of squares of 2^128 to 2^-64.  eps takes the factor
-    // 2^-192 in two steps.
+    // 2^-96 (uniform branch).  The largest row, 32768 elements below 2^128,
+    // sums up to less than 2^79 so, and a sum of squares of 2^128 to 2^-64.
+    // eps takes the factor 2^-192 in two steps.
     float s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
@@ -237,11 +236,11 @@ struct NormBwdParams {
 // stays in registers and goes to the workspace once.  Bound by reading dy, h
 // and dres and writing dx: 8192 x 7168 in 90 us with the partials' sum (5.2
 // TB/s).  A few thousand small rows are bound by the two dependent launches and
-// the partials' way through memory (2352 x 512: 8.7 us, its bytes 2).  Rows wider than 16384 are read twice (the second time from the L2):
-// kept in registers they spill, 2048 x 32768 in 233 us instead of 161.  Two
-// rows at a time, rows kept packed across the barrier and dres
-// loaded before it all took registers that cost a workgroup per CU, and 10 to
-// 60% more time.
+// the partials' way through memory (2352 x 512: 8.7 us, 2 for its bytes).  Rows
+// wider than 16384 are read twice (the second time from the L2): kept in
+// registers they spill, 2048 x 32768 in 233 us instead of 161.  Two rows at a
+// time, rows kept packed across the barrier and dres loaded before it all took
+// registers that cost a workgroup per CU, and 10 to 60% more time.
 template <bool WF32, int CH, bool NT>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdParams p) {
   constexpr bool KEEP = CH < 4;           // a row's chunks fit the registers
