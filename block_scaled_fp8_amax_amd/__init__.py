@@ -15,8 +15,9 @@ import re
 
 import torch
 
-from . import moe
+from . import moe, mxfp4
 from .moe import *  # noqa: F401,F403 - the mixture-of-experts operators (include/fp8blk_moe.h)
+from .mxfp4 import *  # noqa: F401,F403 - MXFP4 experts and the experts' gradients (include/fp8blk_mxfp4.h)
 
 __all__ = [
     "FP8_BLOCK_1x32_E8M0", "FP8_BLOCK_1x128_F32", "FP8_BLOCK_128x128_F32",
@@ -30,7 +31,7 @@ __all__ = [
     "quantize", "dequantize", "fake_quant_merge", "block_scaled_gemm", "grouped_gemm", "lora_backward", "nvfp4_quantize", "nvfp4_dequantize",
     "scale_shape",
     "is_routed_expert_weight", "quantize_state_dict",
-] + moe.__all__
+] + moe.__all__ + mxfp4.__all__
 
 FP8_OK = 0
 FP8_BLOCK_1x32_E8M0, FP8_BLOCK_1x128_F32, FP8_BLOCK_128x128_F32 = 0, 1, 2
@@ -99,6 +100,7 @@ def library():
         if lib.fp8_abi_version() != ABI_VERSION:
             raise ImportError("libfp8blk.so ABI version mismatch")
         moe.declare(lib)
+        mxfp4.declare(lib)
         _lib = lib
     return _lib
 

@@ -179,4 +179,55 @@ struct CombineBwdArgs {
 };
 hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream);
 
+// ------------------------------------------------------------ MXFP4 experts
+
+hipError_t launch_mxfp4_quant(const uint16_t* x, int64_t rows, int64_t cols, bool floor_rule, uint8_t* q,
+                              uint8_t* scale, uint16_t* xdq, hipStream_t stream);
+hipError_t launch_mxfp4_dequant(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, uint16_t* x,
+                                hipStream_t stream);
+
+struct MxProduct {
+  const uint8_t* a;
+  const uint8_t* a_scale;
+  bool a_fp4;
+  int64_t a_rows;
+  const int32_t* row_index;   // null = the row itself
+  const uint8_t* b;
+  const uint8_t* b_scale;
+  const int32_t* offsets;     // null = one group of all rows
+  int groups;
+  int64_t m, n, k;
+  void* y;
+  bool out_f32;
+};
+hipError_t launch_mx_product(const MxProduct& p, int num_cu, hipStream_t stream);
+
+struct MxRows {
+  const uint16_t* x;
+  int64_t x_rows;
+  const int32_t* row_index;   // null = the row itself
+  const uint8_t* q;
+  const uint8_t* scale;
+  const int32_t* offsets;     // null = one group of all rows
+  int64_t groups, total_m, n, k;
+  void* y;
+  bool out_f32;
+};
+hipError_t launch_mx_rows(const MxRows& a, hipStream_t stream);
+
+struct GroupedGrad {
+  const uint16_t* dy;
+  const uint16_t* x;          // wgrad
+  int64_t x_rows;
+  const int32_t* row_index;   // wgrad; null = the row itself
+  const uint16_t* w;          // dgrad
+  const int32_t* offsets;
+  int groups;
+  int64_t total_m, n, k;
+  void* out;
+  bool out_f32;
+};
+hipError_t launch_grouped_dgrad(const GroupedGrad& a, int num_cu, hipStream_t stream);
+hipError_t launch_grouped_wgrad(const GroupedGrad& a, int num_cu, hipStream_t stream);
+
 }  // namespace fp8blk
