@@ -1,6 +1,5 @@
-// Rows of routed experts, as the kernels of the MXFP4 experts find them.
-// The offsets are not checked on the host: group g's rows are [lo, hi) with
-// lo = off[g] and hi = off[g + 1] clamped into [0, total_m] and hi >= lo.
+// Rows of routed experts and the tiles over them, as the kernels of the MXFP4
+// experts find them, and the loads that fill LDS with those tiles.
 #pragma once
 
 #include "device.h"
@@ -9,6 +8,8 @@ namespace fp8blk {
 
 __device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
+// The offsets are not checked on the host: group g's rows are [lo, hi) with
+// lo = off[g] and hi = off[g + 1] clamped into [0, total_m] and hi >= lo.
 __device__ __forceinline__ void rows_of_group(const int32_t* offsets, int g, int total_m, int* lo, int* hi) {
   *lo = clamp_to(offsets[g], 0, total_m);
   *hi = clamp_to(offsets[g + 1], *lo, total_m);
@@ -38,5 +39,136 @@ __device__ __forceinline__ bool row_tile(const int32_t* offsets, int groups, int
   }
   return false;
 }
+
+// Groups are taken in zig-zag order of their index (0, G-1, 1, G-2, ...), so
+// that where sizes fall with the index (experts numbered by popularity) large
+// groups, bound by the matrix cores, run beside small ones, bound by their
+// weights.
+__device__ __forceinline__ int group_at(int place, int groups) {
+  return (place & 1) ? groups - 1 - (place >> 1) : place >> 1;
+}
+
+// Most groups of a call: one int of LDS each.
+constexpr int kMaxGroups = 1024;
+
+// The tiles of a call: every group's rows cut into row tiles of BM, times
+// `tiles_n` column tiles.  Tiles are numbered group by group (in the order
+// above); inside a group in bands of `band` row tiles, column by column, so
+// that consecutive numbers share operands.
+struct TileGrid {
+  const int32_t* offsets;   // null: one group of all rows
+  int groups, total_m, tiles_n, band;
+};
+
+// Row tiles of the groups up to each place, in `upto` (LDS, `groups` ints);
+// returns the number of tiles.  For a workgroup of THREADS threads, all of
+// which have to call it.
+template <int BM, int THREADS>
+__device__ __forceinline__ int count_tiles(const TileGrid& t, int* upto) {
+  if (!t.offsets) return (int)(((int64_t)t.total_m + BM - 1) / BM) * t.tiles_n;
+  constexpr int PER = kMaxGroups / THREADS;
+  const int i = (int)threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int q = i + j * THREADS;
+    if (q >= t.groups) break;
+    int lo, hi;
+    rows_of_group(t.offsets, group_at(q, t.groups), t.total_m, &lo, &hi);
+    upto[q] = (int)(((int64_t)hi - lo + BM - 1) / BM);
+  }
+  __syncthreads();
+  for (int d = 1; d < t.groups; d <<= 1) {
+    int v[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int q = i + j * THREADS;
+      v[j] = q < t.groups && q >= d ? upto[q - d] : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int q = i + j * THREADS;
+      if (q < t.groups) upto[q] += v[j];
+    }
+    __syncthreads();
+  }
+  return upto[t.groups - 1] * t.tiles_n;
+}
+
+struct Tile {
+  int group, row0, rows, col;   // rows: of the tile; col: column tile
+};
+
+// Tile number `id` (below count_tiles' result).  Wave-uniform.
+template <int BM>
+__device__ __forceinline__ Tile tile_at(const TileGrid& t, const int* upto, int id) {
+  int g = 0, before = 0, here, lo = 0, hi = t.total_m;
+  if (t.offsets) {
+    const int slot = id / t.tiles_n;
+    int a = 0, b = t.groups - 1;      // place q with upto[q - 1] <= slot < upto[q]
+    while (a < b) {
+      const int mid = (a + b + 1) >> 1;
+      if (upto[mid - 1] <= slot) a = mid; else b = mid - 1;
+    }
+    before = a > 0 ? upto[a - 1] : 0;
+    here = upto[a] - before;
+    g = group_at(a, t.groups);
+    rows_of_group(t.offsets, g, t.total_m, &lo, &hi);
+  } else {
+    here = (int)(((int64_t)hi + BM - 1) / BM);
+  }
+  const int r = id - before * t.tiles_n;
+  const int band = t.band < here ? t.band : here;
+  const int b = r / (band * t.tiles_n), rr = r - b * (band * t.tiles_n);
+  const int rows_here = here - b * band < band ? here - b * band : band;
+  Tile out;
+  out.group = __builtin_amdgcn_readfirstlane(g);
+  out.row0 = __builtin_amdgcn_readfirstlane(lo + (b * band + rr % rows_here) * BM);
+  out.rows = __builtin_amdgcn_readfirstlane(hi - out.row0 < BM ? hi - out.row0 : BM);
+  out.col = __builtin_amdgcn_readfirstlane(rr / rows_here);
+  return out;
+}
+
+// The `it`-th tile of this workgroup.  Workgroup b runs on XCD b % 8, and the
+// XCDs have L2 caches of their own: each takes runs of consecutive tiles
+// (`per` for each of its workgroups) in turn.
+__device__ __forceinline__ int tile_of_turn(int it, int per) {
+  const int w = (int)(gridDim.x >> 3);
+  return ((it / per) * 8 + (int)(blockIdx.x & 7)) * (per * w) + (it % per) * w + (int)(blockIdx.x >> 3);
+}
+
+// ------------------------------------------------- loads into LDS, and waits
+
+// 16 or 4 bytes per lane from base + voff straight to LDS at lds + 16 (4) *
+// lane; `lds` is wave-uniform.  Counted by vmcnt, in order.
+__device__ __forceinline__ void lds_load16(const void* base, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(lds)
+               : "memory");
+}
+__device__ __forceinline__ void lds_load4(const void* base, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(lds)
+               : "memory");
+}
+// The same through a buffer descriptor: lanes whose 16 bytes lie at or past
+// its length write zeros.
+__device__ __forceinline__ void lds_load16(u32x4 buffer, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(buffer), "s"(lds)
+               : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ void barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Address of a __shared__ object in LDS.
+__device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)p; }
 
 }  // namespace fp8blk
