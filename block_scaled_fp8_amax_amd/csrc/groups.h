@@ -130,10 +130,10 @@ __device__ __forceinline__ Tile tile_at(const TileGrid& t, const int* upto, int 
 }
 
 // The `it`-th tile of this workgroup.  Workgroup b runs on XCD b % 8, and the
-// XCDs have L2 caches of their own: each takes runs of consecutive tiles
-// (`per` for each of its workgroups) in turn.
-__device__ __forceinline__ int tile_of_turn(int it, int per) {
-  const int w = (int)(gridDim.x >> 3);
+// XCDs have L2 caches of their own: each takes runs of consecutive tiles in
+// turn, two for each of its workgroups where there are enough to go round.
+__device__ __forceinline__ int tile_of_turn(int it, int tiles) {
+  const int w = (int)(gridDim.x >> 3), per = tiles >= 4 * (int)gridDim.x ? 2 : 1;
   return ((it / per) * 8 + (int)(blockIdx.x & 7)) * (per * w) + (it % per) * w + (int)(blockIdx.x >> 3);
 }
 
@@ -149,8 +149,13 @@ __device__ __forceinline__ void lds_load4(const void* base, uint32_t voff, uint3
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(lds)
                : "memory");
 }
-// The same through a buffer descriptor: lanes whose 16 bytes lie at or past
-// its length write zeros.
+// The same through a buffer descriptor: lanes whose 16 bytes reach past its
+// length write zeros.
+__device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return (u32x4){(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)), bytes, 0x00027000u};
+}
 __device__ __forceinline__ void lds_load16(u32x4 buffer, uint32_t voff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(buffer), "s"(lds)
                : "memory");

@@ -49,37 +49,42 @@ __device__ __forceinline__ v8i large_codes(v8i c) {
 }
 
 // Tiles.  A workgroup of WM x WN waves makes BM x BN outputs, a wave MI x NI
-// tiles of 16 x 16.  K advances 128 elements a step through a ring of SLOTS
-// stages in LDS that loads fill straight from memory; a row is 64 bytes (E2M1)
-// or 128 (E4M3) of a stage.  16-byte piece c of row r lies at c ^ turn(r), so
-// that the operand reads of 16 rows spread over all banks, whether eight or
-// sixteen lanes are served at once.
+// tiles of 16 x 16.  K advances 256 elements (8 blocks) a stage through a ring
+// of SLOTS stages in LDS that loads fill straight from memory; a row is 128
+// bytes (E2M1) or 256 (E4M3) of a stage.  16-byte piece c of row r lies at
+// c ^ turn(r), so that the 16 rows of an operand read spread over all banks
+// (other turns took twice the time).
 //
-// One barrier a step: at the top of step s every wave has its operands of
-// step s in registers (so stage s may be overwritten) and has waited for its
-// own part of stage s + 1, so behind the barrier stage s + SLOTS is loaded
-// into the place of stage s, and the matrix products of step s run while the
-// operands of step s + 1 are read, each row's into the registers that its
-// products have just left.
+// A stage is two steps of 128 elements.  Which blocks a step takes is free as
+// long as both operands agree: lane l takes block 2 (l / 16) in the first and
+// the block after it in the second, so that the scales of both are two
+// consecutive bytes of a row, read at once, of which the instruction picks the
+// step's.
 //
-// Scales come in chunks of four steps, 16 bytes of a row: a load covers 16
-// rows by four steps of 4 bytes.  A lane reads the byte of its row and block
-// with the operand.
+// While a step's matrix products run, the operands of the next step are read,
+// each row's into the registers that its products have just left.  In the
+// middle of stage s, then, every wave has all of stage s in registers or
+// behind it and waits for its own part of stage s + 1; behind the one barrier
+// there, stage s + SLOTS is loaded into the place of stage s.
+//
+// Scales come for two stages at a time, 16 bytes of a row: a load covers 16
+// rows by four pieces of 4 bytes.
 template <bool FP4>
 __device__ __forceinline__ int turn(int r) {
-  return FP4 ? ((r >> 2) & 3) ^ (r & 2) : (r >> 1) & 7;
+  return FP4 ? (r >> 1) & 7 : r & 15;
 }
 
 template <bool A_FP4, int MI, int NI, int WM, int WN, int SLOTS>
 struct Plan {
   static constexpr int kWaves = WM * WN, BM = 16 * MI * WM, BN = 16 * NI * WN;
-  static constexpr int kARow = A_FP4 ? 64 : 128;
-  static constexpr int kA = BM * kARow, kStage = kA + BN * 64;
-  static constexpr int kLoads = kStage / 1024 / kWaves;          // of a wave and stage
+  static constexpr int kARow = A_FP4 ? 128 : 256;
+  static constexpr int kA = BM * kARow, kStage = kA + BN * 128;
+  static constexpr int kALoads = kA / 1024 / kWaves, kLoads = kStage / 1024 / kWaves;   // of a wave and stage
   static constexpr int kChunk = (BM + BN) * 16;
-  static constexpr int kScaleLoads = kChunk / 256 / kWaves;      // of a wave and chunk
+  static constexpr int kScaleLoads = kChunk / 256 / kWaves;                             // of a wave and chunk
   static constexpr int kScales = SLOTS * kStage, kBytes = kScales + 2 * kChunk;
-  static_assert(kStage % (1024 * kWaves) == 0 && kChunk % (256 * kWaves) == 0 && kScaleLoads <= 4, "shares of the loads");
+  static_assert(kA % (1024 * kWaves) == 0 && kStage % (1024 * kWaves) == 0 && kChunk % (256 * kWaves) == 0,
+                "shares of the loads");
   static_assert(kBytes + kMaxGroups * 4 <= 160 * 1024, "LDS");
 };
 
@@ -91,18 +96,30 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
   const int t = (int)threadIdx.x, lane = t & 63, r16 = lane & 15, kg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave % WM, wn = wave / WM;
   const uint32_t K = (uint32_t)p.k;
-  const int steps = (int)(K / 128);
+  const int stages = (int)((K + 255) / 256), pieces = (int)(K / 128);
   const uint32_t a_row = A_FP4 ? K / 2 : K, b_row = K / 2, s_row = K / 32;
   const uint32_t lds0 = lds_address(smem);
   const int tiles = count_tiles<P::BM, 64 * P::kWaves>(grid, upto);
-  // where a lane's operands lie in a stage, and its scales in a chunk
-  const uint32_t xa = (uint32_t)((wm * MI * 16 + r16) * P::kARow + (kg ^ turn<A_FP4>(r16)) * 16);
-  const uint32_t wb = (uint32_t)(P::kA + (wn * NI * 16 + r16) * 64 + (kg ^ turn<true>(r16)) * 16);
-  const uint32_t xs = (uint32_t)(P::kScales + (wm * MI * 16 + r16) * 16 + kg);
-  const uint32_t ws = (uint32_t)(P::kScales + (P::BM + wn * NI * 16 + r16) * 16 + kg);
+  // where a lane's operands lie in a stage (rows of 16 tiles keep their turn),
+  // and its scales in a chunk
+  const uint32_t xa0 = A_FP4 ? (uint32_t)((wm * MI * 16 + r16) * 128 + ((2 * kg) ^ turn<true>(r16)) * 16)
+                             : (uint32_t)((wm * MI * 16 + r16) * 256 + ((4 * (kg >> 1) + (kg & 1)) ^ turn<false>(r16)) * 16);
+  const uint32_t xa1 = xa0 ^ (A_FP4 ? 16u : 32u);
+  const uint32_t wb0 = (uint32_t)(P::kA + (wn * NI * 16 + r16) * 128 + ((2 * kg) ^ turn<true>(r16)) * 16);
+  const uint32_t wb1 = wb0 ^ 16u;
+  const uint32_t xs = (uint32_t)(P::kScales + (wm * MI * 16 + r16) * 16 + 2 * kg);
+  const uint32_t ws = (uint32_t)(P::kScales + (P::BM + wn * NI * 16 + r16) * 16 + 2 * kg);
+  // Pieces past K (of a last half stage) are read as zeros, at this offset.
+  // Whether a lane's piece is in the upper half is the same for all its loads:
+  // their rows are a multiple of 16 apart.
+  constexpr uint32_t kNowhere = 0xFFFFFFF0u;
+  constexpr int kAPer = P::kARow / 16;
+  const uint32_t a_past = ((lane % kAPer) ^ turn<A_FP4>(wave * (64 / kAPer) + lane / kAPer)) & (kAPer / 2) ? kNowhere : 0u;
+  const uint32_t b_past = ((lane % 8) ^ turn<true>(wave * 8 + lane / 8)) & 4 ? kNowhere : 0u;
+  static_assert(P::kWaves * (64 / kAPer) % 16 == 0 && P::kWaves * 8 % 16 == 0, "rows of a lane's loads");
 
   for (int it = 0;; ++it) {
-    const int id = tile_of_turn(it, 2);
+    const int id = tile_of_turn(it, tiles);
     if (id >= tiles) break;
     const Tile tile = tile_at<P::BM>(grid, upto, id);
     const int64_t m0 = tile.row0, n0 = (int64_t)tile.col * P::BN;
@@ -113,22 +130,21 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
       r = r < tile.rows ? r : tile.rows - 1;
       return p.row_index ? (uint32_t)clamp_to(p.row_index[m0 + r], 0, (int)p.a_rows - 1) : (uint32_t)r;
     };
-    const uint8_t* a = p.a + (p.row_index ? 0 : m0 * a_row);
+    const u32x4 a = buffer_of(p.a + (p.row_index ? 0 : m0 * a_row), kNowhere);
+    const u32x4 b = buffer_of(p.b + (tile.group * p.n + n0) * b_row, kNowhere);
     const uint8_t* as = p.a_scale + (p.row_index ? 0 : m0 * s_row);
-    const uint8_t* b = p.b + (tile.group * p.n + n0) * b_row;
     const uint8_t* bs = p.b_scale + (tile.group * p.n + n0) * s_row;
     // this wave's loads of a stage: blocks wave, wave + kWaves, ... of 1 KiB
     uint32_t off[P::kLoads], soff[P::kScaleLoads];
 #pragma unroll
     for (int j = 0; j < P::kLoads; ++j) {
       const int blk = j * P::kWaves + wave;
-      if (blk * 1024 < P::kA) {
-        constexpr int per = P::kARow / 16;
-        const int r = blk * (64 / per) + lane / per;
-        off[j] = row_of(r) * a_row + (uint32_t)(((lane % per) ^ turn<A_FP4>(r)) * 16);
+      if (j < P::kALoads) {
+        const int r = blk * (64 / kAPer) + lane / kAPer;
+        off[j] = row_of(r) * a_row + (uint32_t)(((lane % kAPer) ^ turn<A_FP4>(r)) * 16);
       } else {
-        const int r = (blk - P::kA / 1024) * 16 + lane / 4, rr = r < cols ? r : cols - 1;
-        off[j] = (uint32_t)rr * b_row + (uint32_t)(((lane % 4) ^ turn<true>(r)) * 16);
+        const int r = (blk - P::kA / 1024) * 8 + lane / 8, rr = r < cols ? r : cols - 1;
+        off[j] = (uint32_t)rr * b_row + (uint32_t)(((lane % 8) ^ turn<true>(r)) * 16);
       }
     }
 #pragma unroll
@@ -140,9 +156,11 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
         soff[j] = (uint32_t)(r - P::BM < cols ? r - P::BM : cols - 1) * s_row;
       }
     }
+    // Scales past K are those of the row's last piece: of zeros, which only a
+    // NaN among them changes, and that one has made the row's results NaN.
     auto load_scales = [&](int chunk) {
       int s = 4 * chunk + (lane & 3);
-      s = s < steps ? s : steps - 1;
+      s = s < pieces ? s : pieces - 1;
 #pragma unroll
       for (int j = 0; j < P::kScaleLoads; ++j) {
         const int blk = j * P::kWaves + wave;
@@ -151,11 +169,15 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
       }
     };
     auto load_stage = [&](int s, uint32_t slot) {
+      const bool half = 2 * s + 1 == pieces;
+      const uint32_t ap = half ? a_past : 0u, bp = half ? b_past : 0u;
 #pragma unroll
       for (int j = 0; j < P::kLoads; ++j) {
-        const int blk = j * P::kWaves + wave;
-        const bool is_a = blk * 1024 < P::kA;
-        lds_load16(is_a ? a : b, off[j] + (uint32_t)s * (is_a ? P::kARow : 64), lds0 + slot + (uint32_t)blk * 1024);
+        const uint32_t to = lds0 + slot + (uint32_t)(j * P::kWaves + wave) * 1024;
+        if (j < P::kALoads)
+          lds_load16(a, (off[j] + (uint32_t)s * P::kARow) | ap, to);
+        else
+          lds_load16(b, (off[j] + (uint32_t)s * 128) | bp, to);
       }
     };
 
@@ -165,74 +187,97 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
 #pragma unroll
       for (int j = 0; j < NI; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
     typename std::conditional<A_FP4, u32x4, v8i>::type xf[MI];
-    u32x4 wf[NI], wnext[NI];
+    u32x4 w0[NI], w1[NI];
     int sx[MI], sw[NI], swnext[NI];
-    auto read_x = [&](uint32_t slot, uint32_t scale, int i) {
-      sx[i] = smem[scale + xs + (uint32_t)(i * 256)];
-      const uint8_t* at = smem + (slot + xa + (uint32_t)(i * 16 * P::kARow));
-      if constexpr (A_FP4) {
-        xf[i] = *reinterpret_cast<const u32x4*>(at);
-      } else {
-        const uint8_t* up = smem + ((slot + xa + (uint32_t)(i * 16 * P::kARow)) ^ 64u);
-        xf[i] = frag(*reinterpret_cast<const u32x4*>(at), *reinterpret_cast<const u32x4*>(up));
+    auto read_x = [&](uint32_t at, int i) {
+      const u32x4 lo = *reinterpret_cast<const u32x4*>(smem + at + (uint32_t)(i * 16 * P::kARow));
+      if constexpr (A_FP4)
+        xf[i] = lo;
+      else
+        xf[i] = frag(lo, *reinterpret_cast<const u32x4*>(smem + (at ^ 128u) + (uint32_t)(i * 16 * P::kARow)));
+    };
+    auto read_w = [&](u32x4& w, uint32_t at, int i) {
+      w = *reinterpret_cast<const u32x4*>(smem + at + (uint32_t)(i * 2048));
+    };
+    auto read_scale = [&](uint32_t at, int i) -> int {
+      return (int)*reinterpret_cast<const uint16_t*>(smem + at + (uint32_t)(i * 256));
+    };
+    // row i of the products of step STEP of a stage
+    auto multiply = [&](auto step, int i, const u32x4* w) {
+      constexpr int STEP = decltype(step)::value;
+      v8i hi = frag(xf[i]), lo = hi;
+      if constexpr (SPLIT) {
+        hi = large_codes(hi);
+        lo = lo ^ hi;
+      }
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(w[j]), hi, acc[i][j], 4, A_FP4 ? 4 : 0, STEP,
+                                                                     sw[j], STEP, sx[i]);
+        if constexpr (SPLIT)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(w[j]), lo, acc[i][j], 4, 0, STEP, sw[j],
+                                                                       STEP, sx[i]);
       }
     };
-    auto read_w = [&](uint32_t slot, uint32_t scale, int i) {
-      swnext[i] = smem[scale + ws + (uint32_t)(i * 256)];
-      wnext[i] = *reinterpret_cast<const u32x4*>(smem + (slot + wb + (uint32_t)(i * 1024)));
-    };
+
     // the first stages and scales
     load_scales(0);
     load_scales(1);
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i)
-      if (i < steps) load_stage(i, (uint32_t)(i * P::kStage));
-    wait_loads<0>();
+      if (i < stages) load_stage(i, (uint32_t)(i * P::kStage));
+    if (stages >= SLOTS) wait_loads<(SLOTS - 1) * P::kLoads>(); else wait_loads<0>();
     barrier();
 #pragma unroll
-    for (int i = 0; i < MI; ++i) read_x(0, 0, i);
+    for (int i = 0; i < MI; ++i) {
+      read_x(xa0, i);
+      sx[i] = read_scale(xs, i);
+    }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      read_w(0, 0, i);
-      wf[i] = wnext[i];
-      sw[i] = swnext[i];
+      read_w(w0[i], wb0, i);
+      sw[i] = read_scale(ws, i);
     }
 
     uint32_t slot = 0;
-    for (int s = 0; s < steps; ++s) {
-      wait_lds_reads();
-      if (s + SLOTS - 1 < steps) wait_loads<(SLOTS - 2) * P::kLoads>(); else wait_loads<0>();
-      barrier();
-      if (s + SLOTS < steps) load_stage(s + SLOTS, slot);
-      if ((s & 3) == 3) load_scales(s / 4 + 2);
-      slot = slot + P::kStage == SLOTS * P::kStage ? 0u : slot + P::kStage;
-      const uint32_t at = (uint32_t)(((s + 1) >> 2 & 1) * P::kChunk + ((s + 1) & 3) * 4);
+    for (int s = 0; s < stages; ++s) {
+      constexpr int kMult = SPLIT ? 2 * NI : NI, kXReads = A_FP4 ? 1 : 2;
       each<MI>([&](auto ic) {
-        constexpr int i = decltype(ic)::value, w0 = i * NI / MI, w1 = (i + 1) * NI / MI;
-        v8i hi = frag(xf[i]), lo = hi;
-        if constexpr (SPLIT) {
-          hi = large_codes(hi);
-          lo = lo ^ hi;
-        }
+        constexpr int i = decltype(ic)::value, first = i * NI / MI, last = (i + 1) * NI / MI;
+        multiply(std::integral_constant<int, 0>{}, i, w0);
+        read_x(slot + xa1, i);
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(wf[j]), hi, acc[i][j], 4, A_FP4 ? 4 : 0, 0,
-                                                                       sw[j], 0, sx[i]);
-          if constexpr (SPLIT)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(wf[j]), lo, acc[i][j], 4, 0, 0, sw[j], 0,
-                                                                         sx[i]);
-        }
-        read_x(slot, at, i);
+        for (int j = first; j < last; ++j) read_w(w1[j], slot + wb1, j);
+        __builtin_amdgcn_sched_group_barrier(0x008, kMult, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, kXReads + (last - first), 0);
+      });
+      // (the compiler would move products past the barrier and the branches)
 #pragma unroll
-        for (int j = w0; j < w1; ++j) read_w(slot, at, j);
-        __builtin_amdgcn_sched_group_barrier(0x008, SPLIT ? 2 * NI : NI, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, (A_FP4 ? 2 : 3) + 2 * (w1 - w0), 0);
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) asm volatile("" : "+v"(acc[i][j]));
+      wait_lds_reads();
+      if (s + SLOTS - 1 < stages) wait_loads<(SLOTS - 2) * P::kLoads>(); else wait_loads<0>();
+      barrier();
+      if (s + SLOTS < stages) load_stage(s + SLOTS, slot);
+      if (s & 1) load_scales((s + 1) / 2 + 1);
+      slot = slot + P::kStage == SLOTS * P::kStage ? 0u : slot + P::kStage;
+      const uint32_t at = (uint32_t)(((s + 1) >> 1 & 1) * P::kChunk + ((s + 1) & 1) * 8);
+      each<MI>([&](auto ic) {
+        constexpr int i = decltype(ic)::value, first = i * NI / MI, last = (i + 1) * NI / MI;
+        multiply(std::integral_constant<int, 1>{}, i, w1);
+        read_x(slot + xa0, i);
+        sx[i] = read_scale(at + xs, i);
+#pragma unroll
+        for (int j = first; j < last; ++j) {
+          read_w(w0[j], slot + wb0, j);
+          swnext[j] = read_scale(at + ws, j);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, kMult, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, kXReads + 1 + 2 * (last - first), 0);
       });
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        wf[i] = wnext[i];
-        sw[i] = swnext[i];
-      }
+      for (int j = 0; j < NI; ++j) sw[j] = swnext[j];
     }
 
     // lane l holds row l % 16 and columns 4 (l / 16) .. + 3 of each 16 x 16
@@ -265,6 +310,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
         }
       }
     }
+    wait_loads<0>();
+    wait_lds_reads();
     barrier();   // the next tile's loads reuse the stages
   }
 }
@@ -291,14 +338,14 @@ void launch_rule(const MxProduct& p, int num_cu, hipStream_t stream) {
   auto even = [&](int64_t bm, int64_t bn) { return active * ((rows + bm - 1) / bm) * ((p.n + bn - 1) / bn); };
   if constexpr (A_FP4) {
     if (rows > 128 && even(256, 256) >= num_cu)
-      return launch_tiles<A_FP4, SPLIT, 8, 4, 2, 4, 4>(p, tiles(256, 256), num_cu, stream);
+      return launch_tiles<A_FP4, SPLIT, 8, 4, 2, 4, 2>(p, tiles(256, 256), num_cu, stream);
   }
   if (rows > 64 && even(128, 256) >= num_cu)
-    launch_tiles<A_FP4, SPLIT, 4, 4, 2, 4, 4>(p, tiles(128, 256), num_cu, stream);
+    launch_tiles<A_FP4, SPLIT, 4, 4, 2, 4, A_FP4 ? 3 : 2>(p, tiles(128, 256), num_cu, stream);
   else if (rows > 64 && even(128, 128) >= num_cu)
-    launch_tiles<A_FP4, SPLIT, 4, 2, 2, 4, 4>(p, tiles(128, 128), num_cu, stream);
+    launch_tiles<A_FP4, SPLIT, 4, 2, 2, 4, A_FP4 ? 4 : 2>(p, tiles(128, 128), num_cu, stream);
   else
-    launch_tiles<A_FP4, SPLIT, 2, 2, 2, 2, 4>(p, tiles(64, 64), num_cu, stream);
+    launch_tiles<A_FP4, SPLIT, 2, 2, 2, 2, 3>(p, tiles(64, 64), num_cu, stream);
 }
 
 }  // namespace
