@@ -21,6 +21,8 @@ constexpr int64_t kMaxWidth = int64_t(1) << 24;
 // Kernels index blocks of 32 elements with 32 bits; a launch's threads stay
 // below 2^32 too.
 constexpr int64_t kMaxBlocks = (int64_t(1) << 32) - (int64_t(1) << 20);
+// Rows of a gradient's tile are read with 32-bit byte offsets.
+constexpr int64_t kMaxGradWidth = int64_t(1) << 22;
 // x of a matvec is read with 32-bit byte offsets whose top bit is free.
 constexpr int64_t kMaxMatvecX = (int64_t(1) << 30) - 1;
 
@@ -38,7 +40,7 @@ int product_shape(int64_t m, int64_t n, int64_t k, int64_t multiple, int y_type)
 int gradient_shape(int64_t groups, int64_t total_m, int64_t n, int64_t k, int type) {
   if (!valid_type(type)) return FP8_ERR_INVALID_ARG;
   if (groups < 1 || groups > 1024) return FP8_ERR_INVALID_ARG;
-  if (total_m < 0 || total_m > kMaxRows || n < 0 || n > kMaxWidth || k < 0 || k > kMaxWidth || n % 8 || k % 8 ||
+  if (total_m < 0 || total_m > kMaxRows || n < 0 || n > kMaxGradWidth || k < 0 || k > kMaxGradWidth || n % 8 || k % 8 ||
       n * k > kMaxRows)
     return FP8_ERR_SHAPE;
   return FP8_OK;

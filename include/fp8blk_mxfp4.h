@@ -159,7 +159,7 @@ int fp8_mxfp4_grouped_matvec(const uint16_t* x, int64_t x_rows, const int32_t* r
  * dy [total_m x n] bf16; w [groups x n x k] bf16; dx [total_m x k] out, bf16
  * or float per dx_type (all 16-byte aligned).
  * Shape: 1 <= groups <= 1024, 0 <= total_m < 2^31, n % 8 == 0, k % 8 == 0,
- *        0 <= n, k <= 2^24, n * k < 2^31.  total_m == 0 or k == 0 enqueues
+ *        0 <= n, k <= 2^22, n * k < 2^31.  total_m == 0 or k == 0 enqueues
  *        nothing; n == 0 writes zeros.
  */
 int fp8_grouped_dgrad(const uint16_t* dy, const uint16_t* w, const int32_t* group_offsets, int64_t groups,
@@ -176,7 +176,7 @@ int fp8_grouped_dgrad(const uint16_t* dy, const uint16_t* w, const int32_t* grou
  * dy [total_m x n] bf16; x [x_rows x k] bf16 (the fake-quant activations);
  * dw [groups x n x k] out, bf16 or float per dw_type (all 16-byte aligned).
  * Shape: 1 <= groups <= 1024, 0 <= total_m < 2^31, n % 8 == 0, k % 8 == 0,
- *        0 <= n, k <= 2^24, n * k < 2^31, x_rows >= 1 where there are rows,
+ *        0 <= n, k <= 2^22, n * k < 2^31, x_rows >= 1 where there are rows,
  *        with row_index x_rows * k < 2^31.  n == 0 or k == 0 enqueues
  *        nothing.
  */

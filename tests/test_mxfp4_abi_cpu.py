@@ -101,7 +101,7 @@ def test_gradient_validation(lib):
     for c in (back, wg):
         assert c(t=2) == INVALID and c(groups=0) == INVALID and c(groups=1025) == INVALID
         assert c(n=60) == SHAPE and c(k=4) == SHAPE and c(n=-8) == SHAPE and c(m=-1) == SHAPE and c(m=1 << 31) == SHAPE
-        assert c(n=1 << 16, k=1 << 15) == SHAPE and c(n=(1 << 24) + 8, k=8) == SHAPE
+        assert c(n=1 << 16, k=1 << 15) == SHAPE and c(n=(1 << 22) + 8, k=8) == SHAPE and c(k=(1 << 22) + 8, n=8) == SHAPE
         assert c(dy=None) == INVALID and c(off=None) == INVALID and c(dy=P + 8) == ALIGN and c(off=P + 2) == ALIGN
         assert c(k=0, dy=None) == OK
     assert back(w=None) == INVALID and back(dx=None) == INVALID and back(w=P + 8) == ALIGN and back(dx=P + 8) == ALIGN
