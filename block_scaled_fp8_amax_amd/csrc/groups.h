@@ -15,27 +15,36 @@ __device__ __forceinline__ void rows_of_group(const int32_t* offsets, int g, int
   *hi = clamp_to(offsets[g + 1], *lo, total_m);
 }
 
-// Row tile `tile` (of `per` rows) counted over all groups: its group, first
-// row and last row; false where there are fewer.
-__device__ __forceinline__ bool row_tile(const int32_t* offsets, int groups, int total_m, int per, int tile, int* g,
-                                         int* first, int* last) {
-  if (!offsets) {
-    *g = 0;
-    *first = tile * per;
-    *last = total_m - *first < per ? total_m : *first + per;
-    return *first < total_m;
-  }
-  for (int e = 0; e < groups; ++e) {
-    int lo, hi;
-    rows_of_group(offsets, e, total_m, &lo, &hi);
-    const int tiles = (hi - lo + per - 1) / per;
-    if (tile < tiles) {
-      *g = e;
-      *first = lo + tile * per;
-      *last = hi - *first < per ? hi : *first + per;
-      return true;
+// The ordinal-th group with rows, and these; false where there are fewer.  For
+// one wave, which looks at 256 groups at a time.
+__device__ __forceinline__ bool nth_group(const int32_t* offsets, int groups, int total_m, int ordinal, int* g, int* lo,
+                                          int* hi) {
+  const int lane = (int)threadIdx.x & 63;
+  int seen = 0;
+  for (int b = 0; b < groups; b += 256) {
+    int l[4], h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = b + i * 64 + lane, at = e < groups ? e : groups - 1;
+      l[i] = offsets[at];
+      h[i] = offsets[at + 1];
     }
-    tile -= tiles;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      l[i] = clamp_to(l[i], 0, total_m);
+      h[i] = b + i * 64 + lane < groups ? clamp_to(h[i], l[i], total_m) : l[i];
+      const unsigned long long full = __builtin_amdgcn_ballot_w64(h[i] > l[i]);
+      const int here = __builtin_popcountll(full);
+      if (ordinal < seen + here) {
+        const bool mine = h[i] > l[i] && __builtin_popcountll(full & ((1ull << lane) - 1)) == ordinal - seen;
+        const int src = __builtin_ctzll(__builtin_amdgcn_ballot_w64(mine));
+        *g = b + i * 64 + src;
+        *lo = __builtin_amdgcn_readlane(l[i], src);
+        *hi = __builtin_amdgcn_readlane(h[i], src);
+        return true;
+      }
+      seen += here;
+    }
   }
   return false;
 }
@@ -155,6 +164,10 @@ __device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
   return (u32x4){(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
                  (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)), bytes, 0x00027000u};
+}
+__device__ __forceinline__ void lds_load4(u32x4 buffer, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(buffer), "s"(lds)
+               : "memory");
 }
 __device__ __forceinline__ void lds_load16(u32x4 buffer, uint32_t voff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(buffer), "s"(lds)

@@ -214,6 +214,9 @@ struct MxRows {
   bool out_f32;
 };
 hipError_t launch_mx_rows(const MxRows& a, hipStream_t stream);
+// A product of few rows (of each group), for which launch_mx_product's tiles
+// are too large.
+hipError_t launch_mx_few(const MxProduct& p, hipStream_t stream);
 
 struct GroupedGrad {
   const uint16_t* dy;

@@ -81,10 +81,9 @@ struct Plan {
   static constexpr int kA = BM * kARow, kStage = kA + BN * 128;
   static constexpr int kALoads = kA / 1024 / kWaves, kLoads = kStage / 1024 / kWaves;   // of a wave and stage
   static constexpr int kChunk = (BM + BN) * 16;
-  static constexpr int kScaleLoads = kChunk / 256 / kWaves;                             // of a wave and chunk
+  static constexpr int kScaleLoads = (kChunk / 256 + kWaves - 1) / kWaves;              // of a wave and chunk, at most
   static constexpr int kScales = SLOTS * kStage, kBytes = kScales + 2 * kChunk;
-  static_assert(kA % (1024 * kWaves) == 0 && kStage % (1024 * kWaves) == 0 && kChunk % (256 * kWaves) == 0,
-                "shares of the loads");
+  static_assert(kA % (1024 * kWaves) == 0 && kStage % (1024 * kWaves) == 0, "shares of the loads");
   static_assert(kBytes + kMaxGroups * 4 <= 160 * 1024, "LDS");
 };
 
@@ -164,8 +163,9 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
 #pragma unroll
       for (int j = 0; j < P::kScaleLoads; ++j) {
         const int blk = j * P::kWaves + wave;
-        lds_load4(blk * 16 < P::BM ? as : bs, soff[j] + (uint32_t)s * 4,
-                  lds0 + P::kScales + (uint32_t)((chunk & 1) * P::kChunk + blk * 256));
+        if (blk * 256 < P::kChunk)
+          lds_load4(blk * 16 < P::BM ? as : bs, soff[j] + (uint32_t)s * 4,
+                    lds0 + P::kScales + (uint32_t)((chunk & 1) * P::kChunk + blk * 256));
       }
     };
     auto load_stage = [&](int s, uint32_t slot) {
@@ -327,30 +327,63 @@ void launch_tiles(const MxProduct& p, int64_t tiles, int num_cu, hipStream_t str
                      stream, p, g);
 }
 
+// The tile of a call, from the rows of a group if they are spread evenly over
+// as many groups as there can be, and the tiles that makes.  Large tiles read
+// less; small ones fill the CUs.  Measured (us, bf16 results; E4M3 / E2M1 rows):
+//   256 x 256, E2M1 only: 16384 rows on 64 experts of 4096 x 4096: 259, 128 x
+//     256: 270;
+//   128 x 256, from three quarters of the CUs on: 1500 x 4096 x 2048: 19.9 /
+//     16.7, 128 x 128: 23.3 / 17.4; at half (2048 x 2048 x 4096) 30.8 / 24.0 and
+//     21.5 / 18.2;
+//   64 x 256 for up to 64 rows, 32 x 128 for up to 32: 2048 rows on 64 experts
+//     of 4096 x 4096: 149 / 145 and 151 / 136, 64 x 64: 176 / 154; 1024 rows on
+//     32: 73 / 69, 67 / 65 and 95 / 84;
+//   64 x 64 by eight waves: 256 x 2048 x 7168: 15.3 / 13.8, by four 18.0 / 15.4.
+// Float results of E4M3 rows, whose operands take twice the registers and
+// products: 64 x 256 (2048 x 2048 x 4096: 34.5, 128 x 128: 40.5, 128 x 256:
+// 55.9) or 32 x 128 (1009 x 2002 x 5120: 29.5, 64 x 64: 31.4).
 template <bool A_FP4, bool SPLIT>
 void launch_rule(const MxProduct& p, int num_cu, hipStream_t stream) {
-  // tiles if the rows are spread evenly over as many groups as there can be
   const int64_t active = p.offsets ? (p.groups < p.m ? p.groups : p.m) : 1;
   const int64_t rows = (p.m + active - 1) / active;
-  auto tiles = [&](int64_t bm, int64_t bn) {
-    return (p.offsets ? p.m / bm + p.groups : (p.m + bm - 1) / bm) * ((p.n + bn - 1) / bn);
+  auto most = [&](int64_t bm, int64_t bn) {     // tiles at most
+    return (p.offsets ? p.m / bm + active : (p.m + bm - 1) / bm) * ((p.n + bn - 1) / bn);
   };
-  auto even = [&](int64_t bm, int64_t bn) { return active * ((rows + bm - 1) / bm) * ((p.n + bn - 1) / bn); };
-  if constexpr (A_FP4) {
-    if (rows > 128 && even(256, 256) >= num_cu)
-      return launch_tiles<A_FP4, SPLIT, 8, 4, 2, 4, 2>(p, tiles(256, 256), num_cu, stream);
+  auto fills = [&](int64_t bm, int64_t bn) {
+    return 4 * active * ((rows + bm - 1) / bm) * ((p.n + bn - 1) / bn) >= 3 * num_cu;
+  };
+  if constexpr (SPLIT) {
+    if (rows > 32 && fills(64, 256))
+      launch_tiles<A_FP4, SPLIT, 2, 4, 2, 4, 2>(p, most(64, 256), num_cu, stream);
+    else
+      launch_tiles<A_FP4, SPLIT, 1, 4, 2, 2, 2>(p, most(32, 128), num_cu, stream);
+  } else {
+    if constexpr (A_FP4) {
+      if (rows > 128 && fills(256, 256))
+        return launch_tiles<A_FP4, SPLIT, 8, 4, 2, 4, 2>(p, most(256, 256), num_cu, stream);
+    }
+    if (rows > 64 && fills(128, 256))
+      launch_tiles<A_FP4, SPLIT, 4, 4, 2, 4, A_FP4 ? 3 : 2>(p, most(128, 256), num_cu, stream);
+    else if (rows > 64 && fills(128, 128))
+      launch_tiles<A_FP4, SPLIT, 4, 2, 2, 4, A_FP4 ? 4 : 2>(p, most(128, 128), num_cu, stream);
+    else if (rows > 32 && rows <= 64 && fills(64, 256))
+      launch_tiles<A_FP4, SPLIT, 2, 4, 2, 4, 3>(p, most(64, 256), num_cu, stream);
+    else if (rows <= 32 && fills(32, 128))
+      launch_tiles<A_FP4, SPLIT, 1, 4, 2, 2, 2>(p, most(32, 128), num_cu, stream);
+    else
+      launch_tiles<A_FP4, SPLIT, 2, 1, 2, 4, 3>(p, most(64, 64), num_cu, stream);
   }
-  if (rows > 64 && even(128, 256) >= num_cu)
-    launch_tiles<A_FP4, SPLIT, 4, 4, 2, 4, A_FP4 ? 3 : 2>(p, tiles(128, 256), num_cu, stream);
-  else if (rows > 64 && even(128, 128) >= num_cu)
-    launch_tiles<A_FP4, SPLIT, 4, 2, 2, 4, A_FP4 ? 4 : 2>(p, tiles(128, 128), num_cu, stream);
-  else
-    launch_tiles<A_FP4, SPLIT, 2, 2, 2, 2, 3>(p, tiles(64, 64), num_cu, stream);
 }
 
 }  // namespace
 
+// Few rows: the kernel that cuts K instead (us, E4M3 / E2M1; dense 64 x 4096 x
+// 7168: 11.2 / 9.1, tiles 15.6 / 13.9, 128 rows: 18.5 / 14.7 and 15.6 / 13.9;
+// 512 rows on 60 of 64 experts of 4096 x 4096: 131 / 125, tiles 137 / 126, 1024
+// rows on 32: 122 / 120, tiles 67 / 65).
 hipError_t launch_mx_product(const MxProduct& p, int num_cu, hipStream_t stream) {
+  const int64_t active = p.offsets ? (p.groups < p.m ? p.groups : p.m) : 1;
+  if (p.offsets ? p.m <= 8 * active : ((p.m + 15) / 16) * ((p.n + 15) / 16) <= 4 * num_cu) return launch_mx_few(p, stream);
   if (p.a_fp4)
     launch_rule<true, false>(p, num_cu, stream);
   else if (p.out_f32)
