@@ -204,3 +204,64 @@ def test_rows_do_not_depend_on_other_rows():
     p = torch.randperm(300, device="cuda", generator=_gen(6))
     z = fb.mxfp4_gemm(a.view(torch.uint8)[p], s[p], "e4m3", b, bs)
     assert torch.equal(z, y[p])
+
+
+@pytest.mark.parametrize("m,n,k,elem,dtype", [
+    (8192, 8192, 128, "e4m3", torch.bfloat16), (8192, 8192, 384, "e2m1", torch.bfloat16),
+    (8100, 8200, 640, "e4m3", torch.bfloat16), (8192, 8192, 1152, "e2m1", torch.float32),
+    (4200, 8194, 896, "e4m3", torch.float32), (8192, 8190, 1024, "e2m1", torch.bfloat16),
+    (4096, 8192, 1664, "e4m3", torch.float32)])
+def test_many_tiles_of_every_length(m, n, k, elem, dtype):
+    """Several tiles for each workgroup: whole ones, cut ones and odd widths follow each other."""
+    g = _gen(m + n + k)
+    a, s, b, bs = _grid(g, m, n, k, elem)
+    y = torch.empty(m, n, dtype=dtype, device="cuda")
+    fb.fp8_mxfp4_gemm(a, s, elem, b, bs, y)
+    want = _rows(a, s, elem) @ _matrix(b, bs).T
+    assert torch.equal(y, want.to(torch.float32).to(dtype))
+
+
+@pytest.mark.parametrize("elem,gather", [("e4m3", False), ("e4m3", True), ("e2m1", True)])
+def test_many_grouped_tiles(elem, gather):
+    """Groups of a few tiles each, whole and cut, empty ones between, and rows behind the last group."""
+    groups, n, k, behind = 40, 2048, 640, 5
+    sizes = [(0, 1, 130, 256, 512, 700, 33, 384)[i % 8] for i in range(groups)]
+    total = sum(sizes) + behind
+    g = _gen(groups)
+    rows = 600 if gather else total
+    a, s, b, bs = _grid(g, rows, n, k, elem, groups)
+    index = torch.randint(0, rows, (total,), device="cuda", generator=g, dtype=torch.int32) if gather else None
+    offsets = torch.tensor([0] + list(np.cumsum(sizes)), dtype=torch.int32, device="cuda")
+    y = torch.full((total, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    fb.fp8_mxfp4_grouped_gemm(a, s, elem, index, b, bs, offsets, y)
+    x = _rows(a, s, elem)
+    x = x[index.long()] if gather else x
+    at = 0
+    for e, size in enumerate(sizes):
+        want = (x[at:at + size] @ _matrix(b[e], bs[e]).T).to(torch.float32).to(torch.bfloat16)
+        assert torch.equal(y[at:at + size], want), e
+        at += size
+    assert bool((y[at:] == 7.0).all())
+
+
+@pytest.mark.parametrize("elem", ["e4m3", "e2m1"])
+def test_rows_past_32_bits(elem):
+    """Few rows, the last of them 4 GiB and more into the operand; ones at a few places of each row."""
+    k, n = 1 << 24, 16
+    m = 262 if elem == "e4m3" else 518
+    g = _gen(7)
+    q = torch.zeros((m, k if elem == "e4m3" else k // 2), dtype=torch.uint8, device="cuda")
+    places = torch.randint(0, k // 2, (m, 8), device="cuda", generator=g) * 2      # even: the low half of an E2M1 byte
+    places[:, 7] = k - 2
+    one = 0x38 if elem == "e4m3" else 0x02
+    q.scatter_(1, places if elem == "e4m3" else places // 2, one)
+    a = q.view(torch.float8_e4m3fn) if elem == "e4m3" else q
+    s = torch.full((m, k // 32), 127, dtype=torch.uint8, device="cuda")
+    b = _bytes(g, n, k // 2)
+    bs = torch.full((n, k // 32), 127, dtype=torch.uint8, device="cuda")
+    y = torch.empty(m, n, dtype=torch.float32, device="cuda")
+    fb.fp8_mxfp4_gemm(a, s, elem, b, bs, y)
+    for r in (0, 1, 127, 255, 256, 257, m - 6, m - 1):
+        p = torch.unique(places[r])
+        want = E2M1.to("cuda")[(b[:, p // 2] & 15).long()].sum(1)
+        assert torch.equal(y[r].to(F64), want), r
