@@ -143,7 +143,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
   __shared__ __attribute__((aligned(1024))) uint8_t smem[P::kBytes];
   __shared__ int upto[kMaxGroups];
   const int t = (int)threadIdx.x, lane = t & 63, r16 = lane & 15, kg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave % WM, wn = wave / WM;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave / WN, wn = wave % WN;
   const uint32_t K = (uint32_t)p.k;
   const int stages = (int)((K + 255) / 256), chunks = (stages + P::CHUNK - 1) / P::CHUNK;
   const uint32_t a_row = A_FP4 ? K / 2 : K, b_row = K / 2, s_row = K / 32;
@@ -163,12 +163,11 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
     return rest < P::BN ? (int)rest : P::BN;
   };
   // Rows behind the tile's last, and columns behind y's, lie behind the end of
-  // their buffers, or (gathered) are the last row again; nothing of them is
-  // stored.
+  // their buffers and are read as zeros (or, where that is past 32 bits, as
+  // the first row); nothing of them is stored.
   auto row_of = [&](const Tile& of, int r) -> uint32_t {
     if (!p.row_index) return (uint32_t)r;
-    r = r < of.rows ? r : of.rows - 1;
-    return (uint32_t)clamp_to(p.row_index[(int64_t)of.row0 + r], 0, (int)p.a_rows - 1);
+    return r < of.rows ? (uint32_t)clamp_to(p.row_index[(int64_t)of.row0 + r], 0, (int)p.a_rows - 1) : (uint32_t)p.a_rows;
   };
 
   // What lies past K (in a last half stage) is read as zeros, at this offset.
@@ -183,7 +182,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
   int s_it = -1, s_chunk = chunks;
   Tile s_tile;
   int d_it = -1, d_stage = stages;
-  Tile d_tile, d_before;
+  Tile d_tile;
   u32x4 a, b;
   uint32_t aoff[P::kALoads], boff = 0;
   auto next_stage = [&]() {
@@ -195,7 +194,6 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
       return;
     }
     const Tile of = d_it == s_it ? s_tile : tile_at<P::BM>(grid, upto, id);
-    d_before = d_tile;
     d_tile = of;
     const int64_t n0 = (int64_t)of.col * P::BN;
     a = p.row_index ? buffer_of(p.a, (uint32_t)p.a_rows * a_row) : buffer_of(p.a + of.row0 * (int64_t)a_row, (uint32_t)of.rows * a_row);
@@ -345,24 +343,32 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
   int in_chunk = 0;
   bool stored = false;                 // exactly kStores stores of the tile before went out between the loads
   for (;;) {
+    // Waves whose rows are all behind the tile's last only load.  (Waves 0 to 3,
+    // on a SIMD each, have the first rows.)
+    const Tile here = d_it == it ? d_tile : tile_at<P::BM>(grid, upto, id);
+    const bool busy = wm * MI * 16 < here.rows;
     clear();
     pin();
     for (int s = 0; s < stages; ++s) {
-      each<kProducts>([&](auto qc) {
-        constexpr int q = decltype(qc)::value;
-        multiply(std::integral_constant<int, 0>{}, q / NI, q % NI, x0, w0);
+      if (busy) {
+        each<kProducts>([&](auto qc) {
+          constexpr int q = decltype(qc)::value;
+          multiply(std::integral_constant<int, 0>{}, q / NI, q % NI, x0, w0);
 #pragma unroll
-        for (int r = part(q, kReadSpan, kReads); r < part(q + 1, kReadSpan, kReads); ++r) {
-          if (r == 0 || r > NI)
-            read_x(x1[r ? r - NI : 0], slot + xa1, r ? r - NI : 0);
-          else
-            read_w(w1[r - 1], slot + wb1, r - 1);
-        }
-        load(freed, part(kProducts + q, P::kSpan, P::kLoads), part(kProducts + q + 1, P::kSpan, P::kLoads));
-        __builtin_amdgcn_sched_barrier(0);
-      });
-      pin();
-      wait_lds_reads();
+          for (int r = part(q, kReadSpan, kReads); r < part(q + 1, kReadSpan, kReads); ++r) {
+            if (r == 0 || r > NI)
+              read_x(x1[r ? r - NI : 0], slot + xa1, r ? r - NI : 0);
+            else
+              read_w(w1[r - 1], slot + wb1, r - 1);
+          }
+          load(freed, part(kProducts + q, P::kSpan, P::kLoads), part(kProducts + q + 1, P::kSpan, P::kLoads));
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        pin();
+        wait_lds_reads();
+      } else {
+        load(freed, part(kProducts, P::kSpan, P::kLoads), P::kLoads);
+      }
       if (stored && s < P::kPast) wait_loads<P::kLater + P::kStores>(); else wait_loads<P::kLater>();
       barrier();
       freed = slot;
@@ -374,35 +380,39 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
       }
       next_stage();
       const uint32_t at = place * P::kChunk + ((uint32_t)in_chunk * 8 ^ stage_turn);
-      each<kProducts>([&](auto qc) {
-        constexpr int q = decltype(qc)::value;
-        multiply(std::integral_constant<int, 1>{}, q / NI, q % NI, x1, w1);
+      // The next stage may be of another tile.
+      if (busy || s + 1 == stages) {
+        each<kProducts>([&](auto qc) {
+          constexpr int q = decltype(qc)::value;
+          multiply(std::integral_constant<int, 1>{}, q / NI, q % NI, x1, w1);
 #pragma unroll
-        for (int r = part(q, kReadSpan, kReads); r < part(q + 1, kReadSpan, kReads); ++r) {
-          if (r == 0 || r > NI) {
-            const int i = r ? r - NI : 0;
-            read_x(x0[i], slot + xa0, i);
-            sxnext[i] = read_scale(at + xs, i);
-          } else {
-            read_w(w0[r - 1], slot + wb0, r - 1);
-            swnext[r - 1] = read_scale(at + ws, r - 1);
+          for (int r = part(q, kReadSpan, kReads); r < part(q + 1, kReadSpan, kReads); ++r) {
+            if (r == 0 || r > NI) {
+              const int i = r ? r - NI : 0;
+              read_x(x0[i], slot + xa0, i);
+              sxnext[i] = read_scale(at + xs, i);
+            } else {
+              read_w(w0[r - 1], slot + wb0, r - 1);
+              swnext[r - 1] = read_scale(at + ws, r - 1);
+            }
           }
-        }
-        load(freed, part(q, P::kSpan, P::kLoads), part(q + 1, P::kSpan, P::kLoads));
-        __builtin_amdgcn_sched_barrier(0);
-      });
-      pin();
+          load(freed, part(q, P::kSpan, P::kLoads), part(q + 1, P::kSpan, P::kLoads));
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        pin();
 #pragma unroll
-      for (int i = 0; i < MI; ++i) sx[i] = own(sxnext[i]);
+        for (int i = 0; i < MI; ++i) sx[i] = own(sxnext[i]);
 #pragma unroll
-      for (int j = 0; j < NI; ++j) sw[j] = own(swnext[j]);
+        for (int j = 0; j < NI; ++j) sw[j] = own(swnext[j]);
+      } else {
+        load(freed, 0, part(kProducts, P::kSpan, P::kLoads));
+      }
     }
 
     // Lane l holds of each 16 x 16 row l % 16 and four columns.  Runs that the
     // last column cuts are stored one by one, what is outside into nothing: a
     // branch for each would make most of the kernel's code.
     constexpr int kRun = NI % 2 ? 4 : 8;
-    const Tile here = d_it == it + 1 && tile_of_turn(d_it, tiles) < tiles ? d_before : tile_at<P::BM>(grid, upto, id);
     const int64_t n0 = (int64_t)here.col * P::BN;
     const int cols = columns(here);
     stored = here.rows == P::BM && cols == P::BN;
