@@ -148,7 +148,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
   const int stages = (int)((K + 255) / 256), chunks = (stages + P::CHUNK - 1) / P::CHUNK;
   const uint32_t a_row = A_FP4 ? K / 2 : K, b_row = K / 2, s_row = K / 32;
   const uint32_t lds0 = lds_address(smem);
-  const int tiles = count_tiles<P::BM, 64 * P::kWaves>(grid, upto);
+  const int tiles = __builtin_amdgcn_readfirstlane(count_tiles<P::BM, 64 * P::kWaves>(grid, upto));
   // where a lane's operands lie in a stage (rows of 16 tiles keep their turn),
   // and its scales in a chunk
   const uint32_t xa0 = A_FP4 ? (uint32_t)((wm * MI * 16 + r16) * 128 + ((2 * kg) ^ turn<true>(r16)) * 16)

@@ -195,3 +195,27 @@ def test_large_weights_and_many_groups():
         assert torch.equal(dw[e], (dy[lo:hi].to(F64).T @ x[lo:hi].to(F64)).to(torch.bfloat16)), e
     for e in (1, 599, 601, 1022):
         assert not dw[e].any()
+
+
+@pytest.mark.parametrize("n,k", [(1024, 2048), (1032, 2040)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_many_tiles(n, k, gather):
+    """Several tiles for each workgroup: whole and cut ones, groups of no, one and many stages in turn."""
+    sizes = [(0, 300, 1, 64, 0, 0, 130, 513, 65, 256)[i % 10] for i in range(43)]
+    g = _gen(n + gather)
+    off, total = _offsets(sizes, 3)
+    rows = 500 if gather else total
+    dy, x, w = _small(g, total, n), _small(g, rows, k), _small(g, len(sizes), n, k)
+    index, at = _index(g, rows, total, gather)
+    for dtype in (torch.float32, torch.bfloat16):
+        dx = torch.full((total, k), float("nan"), dtype=dtype, device="cuda")
+        dw = torch.full((len(sizes), n, k), float("nan"), dtype=dtype, device="cuda")
+        fb.fp8_grouped_dgrad(dy, w, off, dx)
+        fb.fp8_grouped_wgrad(dy, x, index, off, dw)
+        lo = 0
+        for e, size in enumerate(sizes):
+            d = dy[lo:lo + size].to(F64)
+            assert torch.equal(dx[lo:lo + size], (d @ w[e].to(F64)).to(dtype)), (e, dtype)
+            assert torch.equal(dw[e], (d.T @ x[at[lo:lo + size]].to(F64)).to(dtype)), (e, dtype)
+            lo += size
+        assert torch.isnan(dx[lo:]).all()
