@@ -21,41 +21,39 @@ __device__ __forceinline__ uint32_t mx4_code(uint32_t amax) {
   return (uint32_t)(c < 0 ? 0 : c);
 }
 
-constexpr int kQThreads = 256, kQU = 2;
+constexpr int kThreads = 256;
 
-// A lane takes 8 elements (16 bytes), four lanes a block.
+// This thread among all of a launch, whose workgroups fill two dimensions.
+__device__ __forceinline__ uint64_t thread_of_launch() {
+  return ((uint64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+}
+
+// A lane takes 8 elements (16 bytes), four lanes a block.  Bound by memory:
+// 131072 x 7168 with fake-quant values, 4.2 GB: 659 us, 6.5 TB/s; two or four
+// times the elements a lane 760, codes stored through the caches 674.
 template <bool FLOOR, bool DQ>
-__global__ __launch_bounds__(kQThreads) void mxfp4_quant_kernel(const u32x4* __restrict__ x, uint64_t chunks,
-                                                               uint32_t* __restrict__ q, uint8_t* __restrict__ scale,
-                                                               u32x4* __restrict__ xdq) {
-  const uint64_t first = (uint64_t)blockIdx.x * (kQThreads * kQU) + threadIdx.x;
-  u32x4 v[kQU];
-#pragma unroll
-  for (int u = 0; u < kQU; ++u) {
-    const uint64_t c = first + u * kQThreads;
-    v[u] = c < chunks ? __builtin_nontemporal_load(x + c) : (u32x4){0u, 0u, 0u, 0u};
-  }
-#pragma unroll
-  for (int u = 0; u < kQU; ++u) {
-    const uint64_t c = first + u * kQThreads;
-    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-    const uint32_t code = mx4_code<FLOOR>(group_max<4>(absmax_bits<4>(w)));
-    const float s = e8m0_val(code);
-    uint32_t o = 0;
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(v2bf, w[0]), s, 0);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(v2bf, w[1]), s, 1);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(v2bf, w[2]), s, 2);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(v2bf, w[3]), s, 3);
-    if (c >= chunks) continue;
-    q[c] = o;
-    if ((threadIdx.x & 3) == 0) scale[c >> 2] = (uint8_t)code;
-    if constexpr (DQ) {
-      const u32x4 d = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, s, 0)),
-                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, s, 1)),
-                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, s, 2)),
-                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, s, 3))};
-      __builtin_nontemporal_store(d, xdq + c);
-    }
+__global__ __launch_bounds__(kThreads) void mxfp4_quant_kernel(const u32x4* __restrict__ x, uint64_t chunks,
+                                                              uint32_t* __restrict__ q, uint8_t* __restrict__ scale,
+                                                              u32x4* __restrict__ xdq) {
+  const uint64_t c = thread_of_launch();
+  const u32x4 v = c < chunks ? __builtin_nontemporal_load(x + c) : (u32x4){0u, 0u, 0u, 0u};
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint32_t code = mx4_code<FLOOR>(group_max<4>(absmax_bits<4>(w)));
+  const float s = e8m0_val(code);
+  uint32_t o = 0;
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(v2bf, w[0]), s, 0);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(v2bf, w[1]), s, 1);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(v2bf, w[2]), s, 2);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(v2bf, w[3]), s, 3);
+  if (c >= chunks) return;
+  __builtin_nontemporal_store(o, q + c);
+  if ((threadIdx.x & 3) == 0) scale[c >> 2] = (uint8_t)code;
+  if constexpr (DQ) {
+    const u32x4 d = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, s, 0)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, s, 1)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, s, 2)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, s, 3))};
+    __builtin_nontemporal_store(d, xdq + c);
   }
 }
 
@@ -64,20 +62,24 @@ __device__ __forceinline__ float e8m0_or_nan(uint32_t code) {
   return code == 255 ? __uint_as_float(0x7FC00000u) : e8m0_val(code);
 }
 
-__global__ __launch_bounds__(kQThreads) void mxfp4_dequant_kernel(const uint32_t* __restrict__ q, uint64_t chunks,
-                                                                 const uint8_t* __restrict__ scale,
-                                                                 u32x4* __restrict__ x) {
-  const uint64_t first = (uint64_t)blockIdx.x * (kQThreads * kQU) + threadIdx.x;
-  uint32_t w[kQU], c8[kQU];
+// Two times 8 elements a lane (114688 x 2048, 595 MB: 91 us, 6.5 TB/s; once
+// 102, four times 96).
+constexpr int kTimes = 2;
+
+__global__ __launch_bounds__(kThreads) void mxfp4_dequant_kernel(const uint32_t* __restrict__ q, uint64_t chunks,
+                                                                const uint8_t* __restrict__ scale,
+                                                                u32x4* __restrict__ x) {
+  const uint64_t first = (thread_of_launch() - threadIdx.x) * kTimes + threadIdx.x;
+  uint32_t w[kTimes], c8[kTimes];
 #pragma unroll
-  for (int u = 0; u < kQU; ++u) {
-    const uint64_t at = first + u * kQThreads, c = at < chunks ? at : chunks - 1;
+  for (int u = 0; u < kTimes; ++u) {
+    const uint64_t at = first + u * kThreads, c = at < chunks ? at : chunks - 1;
     w[u] = __builtin_nontemporal_load(q + c);
     c8[u] = scale[c >> 2];
   }
 #pragma unroll
-  for (int u = 0; u < kQU; ++u) {
-    const uint64_t c = first + u * kQThreads;
+  for (int u = 0; u < kTimes; ++u) {
+    const uint64_t c = first + u * kThreads;
     if (c >= chunks) continue;
     const float s = e8m0_or_nan(c8[u]);
     const u32x4 d = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[u], s, 0)),
@@ -88,31 +90,36 @@ __global__ __launch_bounds__(kQThreads) void mxfp4_dequant_kernel(const uint32_t
   }
 }
 
+// Workgroups for `threads` (fewer than 2^32 threads may be in a dimension).
+dim3 grid_of(uint64_t threads) {
+  const uint64_t groups = (threads + kThreads - 1) / kThreads, wide = uint64_t(1) << 20;
+  return groups <= wide ? dim3((unsigned)groups) : dim3((unsigned)wide, (unsigned)((groups + wide - 1) / wide));
+}
+
 }  // namespace
 
 hipError_t launch_mxfp4_quant(const uint16_t* x, int64_t rows, int64_t cols, bool floor_rule, uint8_t* q,
                               uint8_t* scale, uint16_t* xdq, hipStream_t stream) {
   const uint64_t chunks = (uint64_t)rows * (uint64_t)(cols / 8);
-  const dim3 grid((unsigned)((chunks + kQThreads * kQU - 1) / (kQThreads * kQU)));
+  const dim3 grid = grid_of(chunks);
   const u32x4* xv = reinterpret_cast<const u32x4*>(x);
   uint32_t* qv = reinterpret_cast<uint32_t*>(q);
   u32x4* dv = reinterpret_cast<u32x4*>(xdq);
   if (floor_rule && xdq)
-    hipLaunchKernelGGL((mxfp4_quant_kernel<true, true>), grid, dim3(kQThreads), 0, stream, xv, chunks, qv, scale, dv);
+    hipLaunchKernelGGL((mxfp4_quant_kernel<true, true>), grid, dim3(kThreads), 0, stream, xv, chunks, qv, scale, dv);
   else if (floor_rule)
-    hipLaunchKernelGGL((mxfp4_quant_kernel<true, false>), grid, dim3(kQThreads), 0, stream, xv, chunks, qv, scale, dv);
+    hipLaunchKernelGGL((mxfp4_quant_kernel<true, false>), grid, dim3(kThreads), 0, stream, xv, chunks, qv, scale, dv);
   else if (xdq)
-    hipLaunchKernelGGL((mxfp4_quant_kernel<false, true>), grid, dim3(kQThreads), 0, stream, xv, chunks, qv, scale, dv);
+    hipLaunchKernelGGL((mxfp4_quant_kernel<false, true>), grid, dim3(kThreads), 0, stream, xv, chunks, qv, scale, dv);
   else
-    hipLaunchKernelGGL((mxfp4_quant_kernel<false, false>), grid, dim3(kQThreads), 0, stream, xv, chunks, qv, scale, dv);
+    hipLaunchKernelGGL((mxfp4_quant_kernel<false, false>), grid, dim3(kThreads), 0, stream, xv, chunks, qv, scale, dv);
   return hipGetLastError();
 }
 
 hipError_t launch_mxfp4_dequant(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, uint16_t* x,
                                 hipStream_t stream) {
   const uint64_t chunks = (uint64_t)rows * (uint64_t)(cols / 8);
-  const dim3 grid((unsigned)((chunks + kQThreads * kQU - 1) / (kQThreads * kQU)));
-  hipLaunchKernelGGL(mxfp4_dequant_kernel, grid, dim3(kQThreads), 0, stream, reinterpret_cast<const uint32_t*>(q),
+  hipLaunchKernelGGL(mxfp4_dequant_kernel, grid_of((chunks + kTimes - 1) / kTimes), dim3(kThreads), 0, stream, reinterpret_cast<const uint32_t*>(q),
                      chunks, scale, reinterpret_cast<u32x4*>(x));
   return hipGetLastError();
 }
