@@ -401,8 +401,8 @@ void launch_tiles(const GroupedGrad& a, int64_t row_tiles, int num_cu, hipStream
 }  // namespace
 
 // Tiles of 256 x 256 by eight waves from one to a CU on, for more than 128 rows
-// a group (us, bf16 results: 16384 rows on 32 experts of 4096 x 7168: 1054, tiles
-// of 128 x 128 by four 1640; 4096 rows on 32 of 2048 x 4096: 170 and 147).
+// a group, else of 128 x 128 by four (us, bf16 results: 16384 rows on 32 experts
+// of 4096 x 7168: 1083 and 1201; 4096 rows on 32 of 2048 x 4096: 167 and 140).
 hipError_t launch_grouped_dgrad(const GroupedGrad& a, int num_cu, hipStream_t stream) {
   const int64_t active = a.groups < a.total_m ? a.groups : a.total_m;
   const int64_t rows = (a.total_m + active - 1) / active;
@@ -414,13 +414,14 @@ hipError_t launch_grouped_dgrad(const GroupedGrad& a, int num_cu, hipStream_t st
   return hipGetLastError();
 }
 
-// The same tiles, from one to a CU on (921 rows on 11 experts of 1000 x 1416: 24,
-// of 128 x 128 19).  Float results are slower with loads among their stores:
-// 16384 rows on 32 experts of 4096 x 7168: 1840, by launch_float_wgrad 1620; bf16:
-// 1164 and 1516.
+// The same tiles, the large ones where they fill three quarters of the CUs'
+// turns (us, gathered: 16384 rows on 32 experts of 4096 x 7168: 1160 and 1526;
+// 921 rows on 8 of 1000 x 1416, 192 tiles: 16 and 18; on 11, 264 tiles: 21 and
+// 18).  Float results are slower with loads among their stores: 16384 rows on 32
+// experts of 4096 x 7168: 1840, by launch_float_wgrad 1620; bf16: 1160 and 1516.
 hipError_t launch_grouped_wgrad(const GroupedGrad& a, int num_cu, hipStream_t stream) {
   if (a.out_f32) return launch_float_wgrad(a, num_cu, stream);
-  const bool big = a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256) >= num_cu;
+  const bool big = fills_turns(a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256), num_cu);
   if (a.row_index) {
     if (big) launch_tiles<true, true, 8, 4, 2, 4>(a, 0, num_cu, stream);
     else launch_tiles<true, true, 4, 4, 2, 2>(a, 0, num_cu, stream);

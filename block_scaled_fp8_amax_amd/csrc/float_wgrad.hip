@@ -243,11 +243,12 @@ void launch_tiles(const GroupedGrad& a, int num_cu, hipStream_t stream) {
 
 }  // namespace
 
-// Tiles of 256 x 256 by eight waves from one to a CU on (16384 rows on 32 experts
-// of 4096 x 7168: 1.62 ms, of 128 x 128 by four 2.2; 921 rows on 11 of 1000 x
-// 1416: 26 us and 19).
+// Tiles of 256 x 256 by eight waves where they fill three quarters of the CUs'
+// turns, else of 128 x 128 by four (us, gathered: 16384 rows on 32 experts of
+// 4096 x 7168: 1619 and 2146; 921 rows on 8 of 1000 x 1416, 192 tiles: 18 and 22;
+// on 11, 264 tiles: 28 and 23).
 hipError_t launch_float_wgrad(const GroupedGrad& a, int num_cu, hipStream_t stream) {
-  const bool big = a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256) >= num_cu;
+  const bool big = fills_turns(a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256), num_cu);
   if (a.row_index) {
     if (big) launch_tiles<true, 8, 4, 2, 4, 2>(a, num_cu, stream);
     else launch_tiles<true, 4, 4, 2, 2, 2>(a, num_cu, stream);

@@ -21,6 +21,12 @@ __device__ __forceinline__ void each(F&& f) {
 
 constexpr int kPlaces = 64;   // of a stage
 
+// Whether `tiles`, one to a CU and turn, keep three quarters of the CUs busy.
+inline bool fills_turns(int64_t tiles, int num_cu) {
+  const int64_t turns = (tiles + num_cu - 1) / num_cu;
+  return 4 * tiles >= 3 * turns * num_cu;
+}
+
 // 16-byte pieces of a row of 128 bytes lie at piece ^ turn(row), 32-byte pieces
 // of a place at piece ^ spread(place).
 __device__ __forceinline__ int turn(int r) { return (r >> 1) & 7; }
