@@ -18,8 +18,7 @@ hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 constexpr int64_t kMaxRows = 0x7FFFFFFFll;
 constexpr int64_t kMaxWidth = int64_t(1) << 24;
-// Kernels index blocks of 32 elements with 32 bits; a launch's threads stay
-// below 2^32 too.
+// Blocks of 32 elements of a codec call: their number fits 32 bits.
 constexpr int64_t kMaxBlocks = (int64_t(1) << 32) - (int64_t(1) << 20);
 // Rows of a gradient's tile are read with 32-bit byte offsets.
 constexpr int64_t kMaxGradWidth = int64_t(1) << 22;

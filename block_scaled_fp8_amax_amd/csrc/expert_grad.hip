@@ -74,8 +74,8 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6), wm = wave / WN, wn = wave % WN;
   const int64_t N = a.n, K = a.k;
   const uint32_t lds0 = lds_address(smem);
-  const int tiles =
-      __builtin_amdgcn_readfirstlane(WGRAD ? grid.groups * grid.tiles_n * grid.band : count_tiles<P::BM, 64 * P::kWaves>(grid, upto));
+  int tiles = grid.groups * grid.tiles_n * grid.band;
+  if constexpr (!WGRAD) tiles = __builtin_amdgcn_readfirstlane(count_tiles<P::BM, 64 * P::kWaves>(grid, upto));
   // Where a lane's operands lie in a stage.  Turned ones: piece c of place p
   // at p * row + ((c ^ spread(p)) * 32), of which a lane takes 8 bytes; c's bits
   // above the wave's first piece are added by exclusive or.
@@ -153,7 +153,8 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
           off[j] = (uint32_t)r * (uint32_t)(N * 2) + (uint32_t)(((lane % 8) ^ turn(r)) * 16);
         } else if (j < P::kRLoads) {
           const int p = (j * P::kWaves + wave) * (64 / kRRow) + lane / kRRow;
-          off[j] = (uint32_t)p * (uint32_t)(N * 2) + (uint32_t)(d.row0 * 2) + (uint32_t)(((lane % kRRow) ^ (spread(p) * 2)) * 16);
+          off[j] = (uint32_t)p * (uint32_t)(N * 2) + (uint32_t)(d.row0 * 2) +
+                   (uint32_t)(((lane % kRRow) ^ (spread(p) * 2)) * 16);
         } else {
           const int p = place_of(j - P::kRLoads);
           off[j] = (GATHER ? 0u : (uint32_t)p * (uint32_t)(K * 2)) + (uint32_t)(d.col0 * 2) +
@@ -209,7 +210,8 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
       }
       const int left = x.places - i_stage * kPlaces;
       if (wave != 0) return;
-      const u32x4 from = buffer_of(a.row_index + x.first + (int64_t)i_stage * kPlaces, (uint32_t)(left < kPlaces ? left : kPlaces) * 4);
+      const u32x4 from = buffer_of(a.row_index + x.first + (int64_t)i_stage * kPlaces,
+                                   (uint32_t)(left < kPlaces ? left : kPlaces) * 4);
       lds_load4(from, (uint32_t)lane * 4, lds0 + P::kIndex + to);
     }
   };
@@ -273,8 +275,8 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
   // and (LOAD) the loads of a stage beside all.
   constexpr int kProducts = MI * NI, kSpan = MI > 1 ? kProducts - NI : kProducts;
   auto part = [](int q, int span, int all) { return q < span ? q * all / span : all; };
-  auto step = [&](auto load_too, u32x4* r, const u32x4* c, u32x4* rnext, u32x4* cnext, uint32_t slot, int next, uint32_t freed,
-                  uint32_t indices) {
+  auto step = [&](auto load_too, u32x4* r, const u32x4* c, u32x4* rnext, u32x4* cnext, uint32_t slot, int next,
+                  uint32_t freed, uint32_t indices) {
     each<kProducts>([&](auto qc) {
       constexpr int q = decltype(qc)::value, i = q / NI, j = q % NI;
       acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, c[j]), __builtin_bit_cast(v8bf, r[i]),
@@ -373,7 +375,8 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
           const v4f u = acc[i][j], v = acc[i][j + 1];
           const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16x2(u[0], u[1]), pack_bf16x2(v[0], v[1]), false, false);
           const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16x2(u[2], u[3]), pack_bf16x2(v[2], v[3]), false, false);
-          if (i * 16 < rows && j * 16 < cols) *reinterpret_cast<u32x4*>(out + j * 32 + lane_at) = (u32x4){lo[0], hi[0], lo[1], hi[1]};
+          if (i * 16 < rows && j * 16 < cols)
+            *reinterpret_cast<u32x4*>(out + j * 32 + lane_at) = (u32x4){lo[0], hi[0], lo[1], hi[1]};
         }
       }
     }

@@ -88,7 +88,8 @@ __global__ __launch_bounds__(64 * WM * WN) void float_wgrad_kernel(GroupedGrad a
       if (!GATHER || wave != 0) return;
       const int left = places - s * kPlaces;
       if (left <= 0) return;
-      const u32x4 from = buffer_of(a.row_index + first + (int64_t)s * kPlaces, (uint32_t)(left < kPlaces ? left : kPlaces) * 4);
+      const u32x4 from =
+          buffer_of(a.row_index + first + (int64_t)s * kPlaces, (uint32_t)(left < kPlaces ? left : kPlaces) * 4);
       lds_load4(from, (uint32_t)lane * 4, lds0 + P::kIndex + (uint32_t)(s & 1) * (kPlaces * 4));
     };
     int index[P::kLoads - P::kRLoads];

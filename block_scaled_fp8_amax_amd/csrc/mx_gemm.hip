@@ -174,7 +174,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
   // Whether a lane's pieces are in the upper half is the same for all its
   // loads: their rows are a multiple of 16 apart.
   constexpr uint32_t kNowhere = 0xFFFFFFF0u;
-  const uint32_t a_past = ((lane % P::kAPer) ^ turn<A_FP4>(wave * (64 / P::kAPer) + lane / P::kAPer)) & (P::kAPer / 2) ? kNowhere : 0u;
+  const int a_piece = (lane % P::kAPer) ^ turn<A_FP4>(wave * (64 / P::kAPer) + lane / P::kAPer);
+  const uint32_t a_past = a_piece & (P::kAPer / 2) ? kNowhere : 0u;
   const uint32_t b_past = ((lane % 8) ^ turn<true>(wave * 8 + lane / 8)) & 4 ? kNowhere : 0u;
 
   // The stages to load, and the scales (below), from tile to tile: tiles as
@@ -196,7 +197,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
     const Tile of = d_it == s_it ? s_tile : tile_at<P::BM>(grid, upto, id);
     d_tile = of;
     const int64_t n0 = (int64_t)of.col * P::BN;
-    a = p.row_index ? buffer_of(p.a, (uint32_t)p.a_rows * a_row) : buffer_of(p.a + of.row0 * (int64_t)a_row, (uint32_t)of.rows * a_row);
+    a = p.row_index ? buffer_of(p.a, (uint32_t)p.a_rows * a_row)
+                    : buffer_of(p.a + of.row0 * (int64_t)a_row, (uint32_t)of.rows * a_row);
     b = buffer_of(p.b + (of.group * p.n + n0) * b_row, (uint32_t)columns(of) * b_row);
     // this wave's loads: blocks wave, wave + kWaves, ... of 1 KiB
 #pragma unroll
@@ -339,9 +341,11 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
     sw[i] = own(read_scale(ws + stage_turn, i));
   }
 
-  uint32_t freed = P::kRing - P::kStage, slot = 0, place = 0;        // of the stage being multiplied: its stage, the place of its scales
+  // of the stage being multiplied: its place in the ring, that of its scales;
+  // and the place behind it, that loads fill
+  uint32_t slot = 0, place = 0, freed = P::kRing - P::kStage;
   int in_chunk = 0;
-  bool stored = false;                 // exactly kStores stores of the tile before went out between the loads
+  bool stored = false;                 // kStores stores of the tile before, or more, are behind the last loads
   for (;;) {
     // Waves whose rows are all behind the tile's last only load.  (Waves 0 to 3,
     // on a SIMD each, have the first rows.)

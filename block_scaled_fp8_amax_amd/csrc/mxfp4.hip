@@ -119,8 +119,8 @@ hipError_t launch_mxfp4_quant(const uint16_t* x, int64_t rows, int64_t cols, boo
 hipError_t launch_mxfp4_dequant(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, uint16_t* x,
                                 hipStream_t stream) {
   const uint64_t chunks = (uint64_t)rows * (uint64_t)(cols / 8);
-  hipLaunchKernelGGL(mxfp4_dequant_kernel, grid_of((chunks + kTimes - 1) / kTimes), dim3(kThreads), 0, stream, reinterpret_cast<const uint32_t*>(q),
-                     chunks, scale, reinterpret_cast<u32x4*>(x));
+  hipLaunchKernelGGL(mxfp4_dequant_kernel, grid_of((chunks + kTimes - 1) / kTimes), dim3(kThreads), 0, stream,
+                     reinterpret_cast<const uint32_t*>(q), chunks, scale, reinterpret_cast<u32x4*>(x));
   return hipGetLastError();
 }
 
