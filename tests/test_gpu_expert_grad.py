@@ -219,3 +219,23 @@ def test_many_tiles(n, k, gather):
             assert torch.equal(dw[e], (d.T @ x[at[lo:lo + size]].to(F64)).to(dtype)), (e, dtype)
             lo += size
         assert torch.isnan(dx[lo:]).all()
+
+
+@pytest.mark.parametrize("n,k", [(72, 136), (2048, 4096)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_bf16_weights_without_rows_and_with_nan(n, k, gather):
+    """No rows at all give zeros; what is not finite reaches its own group's matrix only."""
+    g = _gen(15)
+    e = torch.empty((0, n), dtype=torch.bfloat16, device="cuda")
+    dw = torch.full((3, n, k), 7.0, dtype=torch.bfloat16, device="cuda")
+    fb.fp8_grouped_wgrad(e, torch.empty((0, k), dtype=torch.bfloat16, device="cuda"), None,
+                         torch.zeros(4, dtype=torch.int32, device="cuda"), dw)
+    assert not dw.any()
+    off, total = _offsets([20, 13, 0, 140], 3)
+    dy, x = _small(g, total, n), _small(g, total, k)
+    index = torch.arange(total, device="cuda", dtype=torch.int32) if gather else None
+    clean = fb.grouped_wgrad(dy, x, off, row_index=index, out_dtype=torch.bfloat16)
+    dy[25], x[28] = float("nan"), float("inf")
+    dy[total - 3:], x[total - 3:] = float("nan"), float("nan")
+    dw = fb.grouped_wgrad(dy, x, off, row_index=index, out_dtype=torch.bfloat16)
+    assert not torch.isfinite(dw[1]).any() and torch.equal(dw[[0, 2, 3]], clean[[0, 2, 3]])
