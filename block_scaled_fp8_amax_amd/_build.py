@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libfp8blk.so")
 
 SOURCES = ["quantize.hip", "dequant.hip", "merge.hip", "gemm.hip", "lora_bwd.hip", "nvfp4.hip", "rmsnorm.hip", "route.hip",
-           "matvec.hip", "combine.hip", "mxfp4.hip", "mx_gemm.hip", "mx_matvec.hip", "expert_grad.hip", "float_wgrad.hip", "abi.cpp",
+           "matvec.hip", "combine.hip", "mxfp4.hip", "mx_gemm.hip", "mx_matvec.hip", "expert_grad.hip", "abi.cpp",
            "abi_moe.cpp", "abi_mxfp4.cpp"]
 
 # -ffp-contract=off: every fused multiply-add in the kernels is written out

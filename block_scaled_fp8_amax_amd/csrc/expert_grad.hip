@@ -1,12 +1,14 @@
 // Gradients of the experts' products in bf16 (gfx950), grouped:
 //   dgrad: dx[t][j] = sum_n dy[t][n] W[g][n][j]   (rows t of group g)
-//   wgrad: dw[g][i][j] = sum_t dy[t][i] x[row(t)][j]   (to bf16; float_wgrad.hip has floats)
+//   wgrad: dw[g][i][j] = sum_t dy[t][i] x[row(t)][j]
 // by v_mfma_f32_16x16x32_bf16: lane l holds row (column) l % 16 of an operand
 // and the 8 summed places at 8 (l / 16).
 //
 // Of the operands only dgrad's dy has its summed places side by side in
 // memory.  The others lie in LDS as they do in memory, summed places apart,
-// and are read by ds_read_b64_tr_b16, which turns them (turned.h).
+// and are read by ds_read_b64_tr_b16, which turns 4 places by 16 columns of
+// 16 lanes: lane i of the 16 gives the address of 4 columns 4 (i % 4) of place
+// i / 4 and gets the 4 places of column i.
 //
 // Tiles.  A workgroup of WM x WN waves makes BM x BN outputs, a wave MI x NI
 // tiles of 16 x 16.  The sum advances 64 places a stage (two steps of 32)
@@ -27,13 +29,28 @@
 //
 // Places past the sum's end are zeros on both sides: loads past a buffer's
 // length give zeros, and the lengths end where the group (or n) does.
+#include <type_traits>
+
+#include "groups.h"
 #include "launch.h"
-#include "turned.h"
 
 namespace fp8blk {
 
 namespace {
 
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+
+// f(0), ..., f(N - 1) with compile-time arguments.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each<N, I + 1>(f);
+  }
+}
+
+constexpr int kPlaces = 64;   // of a stage
 constexpr int kSlots = 2;     // stages in LDS
 constexpr uint32_t kNowhere = 0xFFFFFFF0u;
 
@@ -52,6 +69,14 @@ struct Plan {
   static_assert(kLoads + kStores < 64, "vmcnt");
   static_assert(kBytes + kMaxGroups * 4 <= 160 * 1024, "LDS");
 };
+
+__device__ __forceinline__ int turn(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int spread(int place) { return (place & 3) | ((place >> 1) & 4); }
+
+__device__ __forceinline__ u32x2 read_turned(uint32_t lds) {
+  typedef __attribute__((address_space(3))) v4s lds_v4s;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)lds));
+}
 
 __device__ __forceinline__ u32x4 uniform(u32x4 v) {
   return (u32x4){(uint32_t)__builtin_amdgcn_readfirstlane((int)v.x), (uint32_t)__builtin_amdgcn_readfirstlane((int)v.y),
@@ -89,15 +114,14 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
     if constexpr (WGRAD) {
       // band row tiles of a group by tiles_n column tiles, in bands of 8 row tiles
       const int per = grid.band * grid.tiles_n, q = id / per, r = id - q * per;
-      const int group = group_at(q, grid.groups);
       int lo, hi;
-      rows_of_group(a.offsets, group, (int)a.total_m, &lo, &hi);
+      rows_of_group(a.offsets, q, (int)a.total_m, &lo, &hi);
       lo = __builtin_amdgcn_readfirstlane(lo);
       hi = __builtin_amdgcn_readfirstlane(hi);
       const int band = grid.band < 8 ? grid.band : 8;
       const int b = r / (band * grid.tiles_n), rr = r - b * (band * grid.tiles_n);
       const int here = grid.band - b * band < band ? grid.band - b * band : band;
-      w.group = __builtin_amdgcn_readfirstlane(group);
+      w.group = __builtin_amdgcn_readfirstlane(q);
       w.row0 = (int64_t)__builtin_amdgcn_readfirstlane(b * band + rr % here) * P::BM;
       w.col0 = (int64_t)__builtin_amdgcn_readfirstlane(rr / here) * P::BN;
       w.rows = N - w.row0 < P::BM ? (int)(N - w.row0) : P::BM;
@@ -132,7 +156,7 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
     if (++d_stage >= d_stages) {
       d_stage = 0;
       for (d_stages = 0; d_stages == 0;) {
-        const int id = tile_of_turn(++d_it, tiles);
+        const int id = tile_of_turn(++d_it);
         if (id >= tiles) break;
         d = work_of(id);
         d_stages = stages_of(d);
@@ -198,7 +222,7 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
       if (++i_stage >= i_stages) {
         i_stage = 0;
         for (i_stages = 0; i_stages == 0;) {
-          const int id = tile_of_turn(++i_it, tiles);
+          const int id = tile_of_turn(++i_it);
           if (id >= tiles) break;
           x = work_of(id);
           i_stages = stages_of(x);
@@ -222,7 +246,7 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
         index[j - P::kRLoads] = *reinterpret_cast<const int*>(smem + P::kIndex + at + place_of(j - P::kRLoads) * 4);
   };
 
-  int it = 0, id = tile_of_turn(0, tiles);
+  int it = 0, id = tile_of_turn(0);
   if (id >= tiles) return;
   constexpr uint32_t kTurn = kPlaces * 4;       // between the places of indices
   uint32_t index_at = 0;                        // of the next stage to load
@@ -352,7 +376,7 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
     // consecutive columns for each, 64 bytes of a row for the four.
     const int row = wm * MI * 16, col = wn * NI * 16;
     const int64_t first = (WGRAD ? (int64_t)here.group * N + here.row0 : here.row0) * K + here.col0 + row * K + col;
-    const bool f32 = !WGRAD && a.out_f32;
+    const bool f32 = a.out_f32;
     const int lane_col = f32 ? kg * 4 : (kg & 1) * 16 + (kg >> 1) * 8;
     const int rows = here.rows - row - r16, cols = here.cols - col - lane_col;     // from the lane's first on
     const uint32_t lane_at = ((uint32_t)r16 * (uint32_t)K + (uint32_t)lane_col) * (f32 ? 4u : 2u);
@@ -381,7 +405,7 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
       }
     }
     stored = stored || (here.rows == P::BM && here.cols == P::BN);
-    id = tile_of_turn(++it, tiles);
+    id = tile_of_turn(++it);
     if (id >= tiles) break;
   }
   wait_loads<0>();   // (of nothing)
@@ -418,13 +442,12 @@ hipError_t launch_grouped_dgrad(const GroupedGrad& a, int num_cu, hipStream_t st
 }
 
 // The same tiles, the large ones where they fill three quarters of the CUs'
-// turns (us, gathered: 16384 rows on 32 experts of 4096 x 7168: 1160 and 1526;
-// 921 rows on 8 of 1000 x 1416, 192 tiles: 16 and 18; on 11, 264 tiles: 21 and
-// 18).  Float results are slower with loads among their stores: 16384 rows on 32
-// experts of 4096 x 7168: 1840, by launch_float_wgrad 1620; bf16: 1160 and 1516.
+// turns (us, gathered, bf16: 16384 rows on 32 experts of 4096 x 7168: 1160 and
+// 1526; 921 rows on 8 of 1000 x 1416, 192 tiles: 16 and 18; on 11, 264 tiles: 21
+// and 18).
 hipError_t launch_grouped_wgrad(const GroupedGrad& a, int num_cu, hipStream_t stream) {
-  if (a.out_f32) return launch_float_wgrad(a, num_cu, stream);
-  const bool big = fills_turns(a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256), num_cu);
+  const int64_t large = a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256), turns = (large + num_cu - 1) / num_cu;
+  const bool big = 4 * large >= 3 * turns * num_cu;
   if (a.row_index) {
     if (big) launch_tiles<true, true, 8, 4, 2, 4>(a, 0, num_cu, stream);
     else launch_tiles<true, true, 4, 4, 2, 2>(a, 0, num_cu, stream);

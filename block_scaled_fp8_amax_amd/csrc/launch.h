@@ -232,7 +232,5 @@ struct GroupedGrad {
 };
 hipError_t launch_grouped_dgrad(const GroupedGrad& a, int num_cu, hipStream_t stream);
 hipError_t launch_grouped_wgrad(const GroupedGrad& a, int num_cu, hipStream_t stream);
-// The latter with float results.
-hipError_t launch_float_wgrad(const GroupedGrad& a, int num_cu, hipStream_t stream);
 
 }  // namespace fp8blk

@@ -189,7 +189,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
   auto next_stage = [&]() {
     if (++d_stage < stages) return;
     d_stage = 0;
-    const int id = tile_of_turn(++d_it, tiles);
+    const int id = tile_of_turn(++d_it);
     if (id >= tiles) {
       a.z = b.z = 0;
       return;
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
   auto next_scales = [&](int place) {
     if (++s_chunk >= chunks) {
       s_chunk = 0;
-      const int id = tile_of_turn(++s_it, tiles);
+      const int id = tile_of_turn(++s_it);
       if (id >= tiles) {
         as.z = bs.z = 0;
       } else {
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
     }
   };
 
-  int it = 0, id = tile_of_turn(0, tiles);
+  int it = 0, id = tile_of_turn(0);
   if (id >= tiles) return;
   next_scales(0);
   next_scales(1);
@@ -447,7 +447,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
       }
     };
     if (p.out_f32) store(reinterpret_cast<float*>(p.y)); else store(reinterpret_cast<uint16_t*>(p.y));
-    id = tile_of_turn(++it, tiles);
+    id = tile_of_turn(++it);
     if (id >= tiles) break;
   }
   wait_loads<0>();   // (of the empty buffers)
