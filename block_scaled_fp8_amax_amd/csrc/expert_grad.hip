@@ -61,7 +61,7 @@ struct Plan {
   static constexpr int kRLoads = kR / 1024 / kWaves, kLoads = kStage / 1024 / kWaves;   // of a wave and stage
   static constexpr int kCLoads = kLoads - kRLoads;
   static constexpr int kIndex = kSlots * kStage, kBytes = kIndex + 2 * kPlaces * 4;
-  static constexpr int kStores = MI * NI / 2;       // the least of a wave and whole tile
+  static constexpr int kStores = MI * NI / 2;       // of a wave and whole tile, bf16 (floats: twice that)
   static constexpr bool kTwice = kWaves <= 4;       // registers for two sets of rows
   static constexpr bool kInAcc = kTwice;            // results in accumulation registers
   static_assert(kR % (1024 * kWaves) == 0 && kStage % (1024 * kWaves) == 0, "shares of the loads");
@@ -90,7 +90,7 @@ struct Work {
   int64_t row0, col0, first;
 };
 
-template <bool WGRAD, bool GATHER, int MI, int NI, int WM, int WN>
+template <bool WGRAD, bool GATHER, bool F32, int MI, int NI, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a, TileGrid grid) {
   using P = Plan<MI, NI, WM, WN>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[P::kBytes];
@@ -376,11 +376,10 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
     // consecutive columns for each, 64 bytes of a row for the four.
     const int row = wm * MI * 16, col = wn * NI * 16;
     const int64_t first = (WGRAD ? (int64_t)here.group * N + here.row0 : here.row0) * K + here.col0 + row * K + col;
-    const bool f32 = a.out_f32;
-    const int lane_col = f32 ? kg * 4 : (kg & 1) * 16 + (kg >> 1) * 8;
+    const int lane_col = F32 ? kg * 4 : (kg & 1) * 16 + (kg >> 1) * 8;
     const int rows = here.rows - row - r16, cols = here.cols - col - lane_col;     // from the lane's first on
-    const uint32_t lane_at = ((uint32_t)r16 * (uint32_t)K + (uint32_t)lane_col) * (f32 ? 4u : 2u);
-    if (f32) {
+    const uint32_t lane_at = ((uint32_t)r16 * (uint32_t)K + (uint32_t)lane_col) * (F32 ? 4u : 2u);
+    if constexpr (F32) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         pin_row(i);
@@ -421,8 +420,14 @@ void launch_tiles(const GroupedGrad& a, int64_t row_tiles, int num_cu, hipStream
   const int64_t per_cu = 160 * 1024 / (P::kBytes + (WGRAD ? 4 : kMaxGroups * 4));
   const int64_t most = (num_cu >= 8 ? num_cu / 8 * 8 : 8) * per_cu;
   const int64_t wgs = tiles < most ? (tiles + 7) / 8 * 8 : most;
-  hipLaunchKernelGGL((expert_grad_kernel<WGRAD, GATHER, MI, NI, WM, WN>), dim3((unsigned)wgs),
-                     dim3(64 * WM * WN), 0, stream, a, g);
+  // (a kernel for either type: one for both has fewer registers to spare, 1250
+  // us for 1150 of gathered bf16 gradients of weights)
+  if (a.out_f32)
+    hipLaunchKernelGGL((expert_grad_kernel<WGRAD, GATHER, true, MI, NI, WM, WN>), dim3((unsigned)wgs),
+                       dim3(64 * WM * WN), 0, stream, a, g);
+  else
+    hipLaunchKernelGGL((expert_grad_kernel<WGRAD, GATHER, false, MI, NI, WM, WN>), dim3((unsigned)wgs),
+                       dim3(64 * WM * WN), 0, stream, a, g);
 }
 
 }  // namespace
