@@ -446,7 +446,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
         }
       }
     };
-    if (p.out_f32) store(reinterpret_cast<float*>(p.y)); else store(reinterpret_cast<uint16_t*>(p.y));
+    // (E4M3 rows: floats exactly where products are split)
+    if (A_FP4 ? p.out_f32 : SPLIT) store(reinterpret_cast<float*>(p.y)); else store(reinterpret_cast<uint16_t*>(p.y));
     id = tile_of_turn(++it);
     if (id >= tiles) break;
   }
