@@ -433,8 +433,8 @@ void launch_tiles(const GroupedGrad& a, int64_t row_tiles, int num_cu, hipStream
 }  // namespace
 
 // Tiles of 256 x 256 by eight waves from one to a CU on, for more than 128 rows
-// a group, else of 128 x 128 by four (us, bf16 results: 16384 rows on 32 experts
-// of 4096 x 7168: 1083 and 1201; 4096 rows on 32 of 2048 x 4096: 167 and 140).
+// a group, else of 128 x 128 by four (us: 16384 rows on 32 experts of 4096 x
+// 7168, bf16, 1017 and 1178; 4096 rows on 32 of 2048 x 4096, float, 171 and 148).
 hipError_t launch_grouped_dgrad(const GroupedGrad& a, int num_cu, hipStream_t stream) {
   const int64_t active = a.groups < a.total_m ? a.groups : a.total_m;
   const int64_t rows = (a.total_m + active - 1) / active;
@@ -447,9 +447,9 @@ hipError_t launch_grouped_dgrad(const GroupedGrad& a, int num_cu, hipStream_t st
 }
 
 // The same tiles, the large ones where they fill three quarters of the CUs'
-// turns (us, gathered, bf16: 16384 rows on 32 experts of 4096 x 7168: 1160 and
-// 1526; 921 rows on 8 of 1000 x 1416, 192 tiles: 16 and 18; on 11, 264 tiles: 21
-// and 18).
+// turns (us, gathered, bf16: 16384 rows on 32 experts of 4096 x 7168: 1130 and
+// 1490; 921 rows on 8 of 1000 x 1416, 192 tiles: 16 and 17; on 11, 264 tiles: 20
+// and 17).
 hipError_t launch_grouped_wgrad(const GroupedGrad& a, int num_cu, hipStream_t stream) {
   const int64_t large = a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256), turns = (large + num_cu - 1) / num_cu;
   const bool big = 4 * large >= 3 * turns * num_cu;
