@@ -528,11 +528,14 @@ void launch_rule(const MxProduct& p, int num_cu, hipStream_t stream) {
 
 }  // namespace
 
-// Few rows: the kernel that cuts K instead (us, E4M3 / E2M1; dense 64 x 4096 x
-// 7168: 11.2 / 9.1, tiles 15.6 / 13.9, 128 rows: 18.5 / 14.7 and 15.6 / 13.9;
-// 512 rows on 60 of 64 experts of 4096 x 4096: 131 / 125, tiles 137 / 126, 1024
-// rows on 32: 122 / 120, tiles 67 / 65).  It finds all rows of A with 32-bit
-// byte offsets.
+// Few rows: the kernel that cuts K instead, up to 8 a group (us, E4M3 / E2M1;
+// dense 64 x 4096 x 7168: 10.7 / 7.6, tiles 16.6 / 14.8, 128 rows: 17.3 / 13.0
+// and 16.6 / 14.8; gathered, 64 rows on 52 of 256 experts of 4096 x 7168: 139 /
+// 138, tiles 166 / 154; 512 on 60 of 64 of 4096 x 4096: 106 / 97, tiles 106 / 98;
+// 1024 on 64: 133 / 120 and 110 / 104).  The host does not know which groups
+// have rows: few rows for 256 groups that 32 of them get go the slower way
+// (2048 rows of 4096 x 7168: 356 / 321, tiles 118 / 101).  The kernel finds all
+// rows of A with 32-bit byte offsets.
 hipError_t launch_mx_product(const MxProduct& p, int num_cu, hipStream_t stream) {
   const int64_t active = p.offsets ? (p.groups < p.m ? p.groups : p.m) : 1;
   const bool few = p.offsets ? p.m <= 8 * active : ((p.m + 15) / 16) * ((p.n + 15) / 16) <= 4 * num_cu;

@@ -109,8 +109,9 @@ __device__ __forceinline__ void multiply_rows(const Rows& a, int grp, int lo, in
   const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(sc) & 3);
   const u32x4 sb = buffer_of(sc - mis, ((uint32_t)cols * s_row + mis + 3u) & ~3u);
   const u32x4 xb = buffer_of(a.x, (uint32_t)(a.x_rows * x_row));
-  const uint32_t xmis = X == kBf16 ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(a.x_scale) & 3);
-  const u32x4 xsb = buffer_of(a.x_scale - xmis, X == kBf16 ? 0u : ((uint32_t)(a.x_rows * s_row) + xmis + 3u) & ~3u);
+  // (quantized rows: K is a multiple of 128 and x_scale 4-byte aligned, so each
+  // row's scales begin a dword)
+  const u32x4 xsb = buffer_of(a.x_scale, X == kBf16 ? 0u : (uint32_t)(a.x_rows * s_row));
 
   const uint32_t ring = lds_address(smem) + (uint32_t)(wave * WAVE);
   const uint8_t* mine = smem + wave * WAVE;
@@ -136,7 +137,7 @@ __device__ __forceinline__ void multiply_rows(const Rows& a, int grp, int lo, in
       xoff[i] = m < mr ? row_of(m) * x_row + (uint32_t)(piece * 16) : kNowhere;
     }
 #pragma unroll
-    for (int c = 0; c < T; ++c) xsoff[c] = X == kBf16 ? 0u : (row_of(c * 16 + srow) * s_row + xmis) & ~3u;
+    for (int c = 0; c < T; ++c) xsoff[c] = X == kBf16 ? 0u : row_of(c * 16 + srow) * s_row;
 
     auto load = [&](int s, int slot) {
       const uint32_t at = ring + (uint32_t)(slot * P::kStage);
@@ -220,8 +221,7 @@ __device__ __forceinline__ void multiply_rows(const Rows& a, int grp, int lo, in
           }
         }
         if constexpr (X != kBf16) {
-          const uint32_t mm = (row_of(c * 16 + r16) * s_row + xmis) & 3u;
-          const uint8_t* sp = at + P::kW + P::kX + P::kWScale + c * 256 + r16 * 16 + mm + 2 * kg;
+          const uint8_t* sp = at + P::kW + P::kX + P::kWScale + c * 256 + r16 * 16 + 2 * kg;
 #pragma unroll
           for (int j = 0; j < 2; ++j) xs[c][j] = b0 + j < blocks ? sp[j] : 127u;
         }
