@@ -139,7 +139,7 @@ __global__ __launch_bounds__(64 * WM * WN) void expert_grad_kernel(GroupedGrad a
     w.cols = K - w.col0 < P::BN ? (int)(K - w.col0) : P::BN;
     return w;
   };
-  auto stages_of = [&](const Work& w) { return (w.places + kPlaces - 1) / kPlaces; };
+  auto stages_of = [&](const Work& w) { return stages_in(w.places, kPlaces); };
 
   // The stages to load, from tile to tile; behind the last they are of nothing.
   constexpr int kCRow = P::BN / 8, kRRow = P::BM / 8;     // 16-byte pieces of a place

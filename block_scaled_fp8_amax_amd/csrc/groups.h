@@ -8,6 +8,9 @@ namespace fp8blk {
 
 __device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
+// Stages of `each` places (or rows) that hold `places` of them, up to 2^31 - 1.
+__host__ __device__ __forceinline__ int stages_in(int places, int each) { return places / each + (places % each != 0); }
+
 // The offsets are not checked on the host: group g's rows are [lo, hi) with
 // lo = off[g] and hi = off[g + 1] clamped into [0, total_m] and hi >= lo.
 __device__ __forceinline__ void rows_of_group(const int32_t* offsets, int g, int total_m, int* lo, int* hi) {
