@@ -55,6 +55,16 @@ __device__ __forceinline__ bool nth_group(const int32_t* offsets, int groups, in
 // Most groups of a call: one int of LDS each.
 constexpr int kMaxGroups = 1024;
 
+// Most tiles that are counted.  Results that fit the GPU's memory have fewer;
+// offsets that fall and rise again, which may name each row many times, would
+// have more than an int counts, and tiles outside the rows with it.
+constexpr int kMostTiles = 1 << 30;
+__host__ __device__ __forceinline__ int add_tiles(int a, int b) { return a < kMostTiles - b ? a + b : kMostTiles; }
+__host__ __device__ __forceinline__ int times_tiles(int a, int b) {
+  const int64_t all = (int64_t)a * b;
+  return all < kMostTiles ? (int)all : kMostTiles;
+}
+
 // The tiles of a call: every group's rows cut into row tiles of BM, times
 // `tiles_n` column tiles.  Tiles are numbered group by group;
 // inside a group in bands of `band` row tiles, column by column, so
@@ -69,7 +79,7 @@ struct TileGrid {
 // which have to call it.
 template <int BM, int THREADS>
 __device__ __forceinline__ int count_tiles(const TileGrid& t, int* upto) {
-  if (!t.offsets) return (int)(((int64_t)t.total_m + BM - 1) / BM) * t.tiles_n;
+  if (!t.offsets) return times_tiles(stages_in(t.total_m, BM), t.tiles_n);
   constexpr int PER = kMaxGroups / THREADS;
   const int i = (int)threadIdx.x;
 #pragma unroll
@@ -78,7 +88,7 @@ __device__ __forceinline__ int count_tiles(const TileGrid& t, int* upto) {
     if (q >= t.groups) break;
     int lo, hi;
     rows_of_group(t.offsets, q, t.total_m, &lo, &hi);
-    upto[q] = (int)(((int64_t)hi - lo + BM - 1) / BM);
+    upto[q] = stages_in(hi - lo, BM);
   }
   __syncthreads();
   for (int d = 1; d < t.groups; d <<= 1) {
@@ -92,11 +102,11 @@ __device__ __forceinline__ int count_tiles(const TileGrid& t, int* upto) {
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int q = i + j * THREADS;
-      if (q < t.groups) upto[q] += v[j];
+      if (q < t.groups) upto[q] = add_tiles(upto[q], v[j]);
     }
     __syncthreads();
   }
-  return upto[t.groups - 1] * t.tiles_n;
+  return times_tiles(upto[t.groups - 1], t.tiles_n);
 }
 
 struct Tile {
@@ -119,7 +129,7 @@ __device__ __forceinline__ Tile tile_at(const TileGrid& t, const int* upto, int 
     g = a;
     rows_of_group(t.offsets, g, t.total_m, &lo, &hi);
   } else {
-    here = (int)(((int64_t)hi + BM - 1) / BM);
+    here = stages_in(hi, BM);
   }
   const int r = id - before * t.tiles_n;
   const int band = t.band < here ? t.band : here;

@@ -432,7 +432,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_gemm_kernel(MxProduct p, Tile
       for (int i = 0; i < MI; ++i) {
         pin_row(i);                               // (few results at a time in registers)
         const int row = (wm * MI + i) * 16;       // the first
-        T* const first = y + (here.row0 + row) * p.n + n0;
+        T* const first = y + ((int64_t)here.row0 + row) * p.n + n0;
         const bool there = row + r16 < here.rows;
 #pragma unroll
         for (int j = 0; j < NI; j += kRun / 4) {
