@@ -11,7 +11,8 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("sizes,n,k", [([1], 40, 2688), ([2, 0, 3, 1, 9, 0], 70, 4224), ([1] * 20 + [17], 33, 2176),
-                                       ([4, 5, 30, 0, 1, 0, 0, 2], 2050, 1920), ([3, 0, 4], 130, 7168)])
+                                       ([4, 5, 30, 0, 1, 0, 0, 2], 2050, 1920), ([3, 0, 4], 130, 7168),
+                                       ([3, 1, 0, 2, 17, 1, 5, 0, 4, 1, 1, 8], 4100, 1664)])
 @pytest.mark.parametrize("elem", ["e4m3", "e2m1"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_gathered_rows_over_many_stages(sizes, n, k, elem, dtype):
