@@ -29,8 +29,6 @@
 //
 // Places past the sum's end are zeros on both sides: loads past a buffer's
 // length give zeros, and the lengths end where the group (or n) does.
-#include <type_traits>
-
 #include "groups.h"
 #include "launch.h"
 
@@ -40,15 +38,6 @@ namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
-
-// f(0), ..., f(N - 1) with compile-time arguments.
-template <int N, int I = 0, typename F>
-__device__ __forceinline__ void each(F&& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>{});
-    each<N, I + 1>(f);
-  }
-}
 
 constexpr int kPlaces = 64;   // of a stage
 constexpr int kSlots = 2;     // stages in LDS

@@ -2,9 +2,20 @@
 // experts find them, and the loads that fill LDS with those tiles.
 #pragma once
 
+#include <type_traits>
+
 #include "device.h"
 
 namespace fp8blk {
+
+// f(0), ..., f(N - 1) with compile-time arguments.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each<N, I + 1>(f);
+  }
+}
 
 __device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
@@ -155,18 +166,9 @@ __device__ __forceinline__ int tile_of_turn(int it) {
 
 // ------------------------------------------------- loads into LDS, and waits
 
-// 16 or 4 bytes per lane from base + voff straight to LDS at lds + 16 (4) *
-// lane; `lds` is wave-uniform.  Counted by vmcnt, in order.
-__device__ __forceinline__ void lds_load16(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "s"(lds)
-               : "memory");
-}
-__device__ __forceinline__ void lds_load4(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "s"(lds)
-               : "memory");
-}
-// The same through a buffer descriptor: lanes whose 16 bytes reach past its
-// length write zeros.
+// A buffer's descriptor, and 16 or 4 bytes per lane from voff on in it straight
+// to LDS at lds + 16 (4) * lane; `lds` is wave-uniform.  Lanes whose bytes reach
+// past the buffer's length write zeros.  Counted by vmcnt, in order.
 __device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
   return (u32x4){(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),

@@ -19,40 +19,13 @@
 // 131072 rows on 256 experts of 4096 x 7168: 3450, 5850).  Float results take
 // two, with the codes of |a| >= 2 and with the others: bits down to 2^-3 under
 // e <= 8 + 2, down to 2^-10 under e <= 0 + 2, so that nothing is lost.
-#include <type_traits>
-
 #include "groups.h"
 #include "launch.h"
+#include "mx.h"
 
 namespace fp8blk {
 
 namespace {
-
-__device__ __forceinline__ v8i frag(u32x4 lo) { return (v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, 0, 0, 0, 0}; }
-__device__ __forceinline__ v8i frag(u32x4 lo, u32x4 hi) {
-  return (v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-}
-
-__device__ __forceinline__ v8i frag(v8i f) { return f; }
-
-// f(0), ..., f(N - 1) with compile-time arguments.
-template <int N, int I = 0, typename F>
-__device__ __forceinline__ void each(F&& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>{});
-    each<N, I + 1>(f);
-  }
-}
-
-// The codes with |a| >= 2 (bit 6 of a byte).
-__device__ __forceinline__ v8i large_codes(v8i c) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t m = ((uint32_t)c[i] >> 6) & 0x01010101u;
-    c[i] &= (int)((m << 8) - m);
-  }
-  return c;
-}
 
 // N consecutive results, at any address that their type may have.
 template <int N>

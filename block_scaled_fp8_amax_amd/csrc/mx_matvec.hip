@@ -16,10 +16,9 @@
 // v_cvt_scalef32_pk_bf16_fp4 makes two of them.  Quantized rows take the
 // scaled product of mx_gemm.hip (where the cut of E4M3 sums is explained).
 // As there, lane l takes blocks 2 (l / 16) and 2 (l / 16) + 1 of a stage.
-#include <type_traits>
-
 #include "groups.h"
 #include "launch.h"
+#include "mx.h"
 
 namespace fp8blk {
 
@@ -38,21 +37,6 @@ __device__ __forceinline__ v8bf decode8(uint32_t c, float s) {
 
 __device__ __forceinline__ float scale_of(uint32_t code) {
   return code == 255 ? __uint_as_float(0x7FC00000u) : e8m0_val(code);
-}
-
-__device__ __forceinline__ v8i operand(u32x4 lo) {
-  return (v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, 0, 0, 0, 0};
-}
-__device__ __forceinline__ v8i operand(u32x4 lo, u32x4 hi) {
-  return (v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-}
-__device__ __forceinline__ v8i large_codes(v8i c) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t m = ((uint32_t)c[i] >> 6) & 0x01010101u;
-    c[i] &= (int)((m << 8) - m);
-  }
-  return c;
 }
 
 enum { kBf16 = 0, kE4m3 = 1, kE4m3Split = 2, kE2m1 = 3 };
@@ -247,18 +231,18 @@ __device__ __forceinline__ void multiply_rows(const Rows& a, int grp, int lo, in
 #pragma unroll
             for (int c = 0; c < T; ++c) {
               if constexpr (X == kE2m1) {
-                acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[r][j]), operand(x[c][j]), acc[r][c],
+                acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(w[r][j]), frag(x[c][j]), acc[r][c],
                                                                              4, 4, 0, (int)ws[r][j], 0, (int)xs[c][j]);
               } else {
-                v8i up = operand(x[c][2 * j], x[c][2 * j + 1]), low = up;
+                v8i up = frag(x[c][2 * j], x[c][2 * j + 1]), low = up;
                 if constexpr (X == kE4m3Split) {
                   up = large_codes(up);
                   low = low ^ up;
                 }
-                acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[r][j]), up, acc[r][c], 4, 0, 0,
+                acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(w[r][j]), up, acc[r][c], 4, 0, 0,
                                                                              (int)ws[r][j], 0, (int)xs[c][j]);
                 if constexpr (X == kE4m3Split)
-                  acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w[r][j]), low, acc[r][c], 4, 0, 0,
+                  acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(w[r][j]), low, acc[r][c], 4, 0, 0,
                                                                                (int)ws[r][j], 0, (int)xs[c][j]);
               }
             }
