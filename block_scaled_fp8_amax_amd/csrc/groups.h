@@ -20,7 +20,9 @@ __device__ __forceinline__ void each(F&& f) {
 __device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
 // Stages of `each` places (or rows) that hold `places` of them, up to 2^31 - 1.
-__host__ __device__ __forceinline__ int stages_in(int places, int each) { return places / each + (places % each != 0); }
+__host__ __device__ __forceinline__ int stages_in(int places, int each) {
+  return (int)(((uint32_t)places + (uint32_t)each - 1u) / (uint32_t)each);
+}
 
 // The offsets are not checked on the host: group g's rows are [lo, hi) with
 // lo = off[g] and hi = off[g + 1] clamped into [0, total_m] and hi >= lo.
