@@ -22,7 +22,9 @@
 // the operands of the next step are read (by eight waves, which have registers
 // for one set of rows, each row's into those that its products have just left),
 // in the middle of a stage one barrier frees it, and stages go on from tile to
-// tile of a workgroup without a pause.
+// tile of a workgroup.  (Wgrad reads the offsets of a new tile's group from
+// memory there, dgrad those of the group it has found in LDS; either waits for
+// what is on its way.)
 //
 // The first operand of a product is the one whose columns are those of the
 // result, so that a lane's four results are consecutive in memory.
@@ -50,7 +52,7 @@ struct Plan {
   static constexpr int kRLoads = kR / 1024 / kWaves, kLoads = kStage / 1024 / kWaves;   // of a wave and stage
   static constexpr int kCLoads = kLoads - kRLoads;
   static constexpr int kIndex = kSlots * kStage, kBytes = kIndex + 2 * kPlaces * 4;
-  static constexpr int kStores = MI * NI / 2;       // of a wave and whole tile, bf16 (floats: twice that)
+  static constexpr int kStores = MI * NI / 2;       // of a wave and whole tile, bf16 (floats: twice that, half of them waited for)
   static constexpr bool kTwice = kWaves <= 4;       // registers for two sets of rows
   static constexpr bool kInAcc = kTwice;            // results in accumulation registers
   static_assert(kR % (1024 * kWaves) == 0 && kStage % (1024 * kWaves) == 0, "shares of the loads");

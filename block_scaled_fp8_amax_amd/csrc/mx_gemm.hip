@@ -15,8 +15,8 @@
 // least normal one; runs and blocks are added in fp32).  E2M1 products have no
 // bit that low.  E4M3 rows lose at most 7 * 2^-12 of a run's largest product so,
 // and bf16 results of them keep it: their operands are known to 2^-4, and one
-// product in place of two is twice the rate (8192 x 8192 x 7168: 348 us, 685;
-// 131072 rows on 256 experts of 4096 x 7168: 3450, 5850).  Float results take
+// product in place of two is twice the rate (8192 x 8192 x 7168: 354 us, 660;
+// 131072 rows on 256 experts of 4096 x 7168: 3440, 6600).  Float results take
 // two, with the codes of |a| >= 2 and with the others: bits down to 2^-3 under
 // e <= 8 + 2, down to 2^-10 under e <= 0 + 2, so that nothing is lost.
 #include "groups.h"
@@ -69,9 +69,12 @@ __device__ __forceinline__ void store_one(__amdgpu_buffer_rsrc_t y, uint16_t, ui
 // its own part of stage s + 1; behind the one barrier there, stage s + SLOTS is
 // loaded into the place of stage s.
 //
-// Stages go on from tile to tile of a workgroup without a pause: while one
-// tile ends, loads are for the next.  Behind the last tile they find an empty
-// buffer, which costs nothing and keeps their number the same.
+// Stages go on from tile to tile of a workgroup: while one tile ends, loads are
+// for the next.  Behind the last tile they find an empty buffer, which costs
+// nothing and keeps their number the same.  A new tile's group, and the indices
+// of gathered rows, are read where its first loads are formed, and each of those
+// reads waits for all that is on its way (131072 E4M3 rows on 256 experts of
+// 4096 x 7168: 3510 us gathered, 3457 without an index).
 //
 // Scales come for CHUNK stages at a time, 8 CHUNK bytes of a row, into two
 // places in turn.  (Each row touched takes a cache line's time, so that CHUNK
@@ -449,7 +452,9 @@ void launch_tiles(const MxProduct& p, int64_t tiles, int num_cu, hipStream_t str
 // less; small ones fill the CUs.  Measured (us, bf16 results; E4M3 / E2M1 rows):
 //   256 x 256 by four waves, E2M1 only, from 1024 rows on: 8192 x 8192 x 7168:
 //     247, 128 x 256: 266; 512 rows on each of 64 experts of 4096 x 7168: 692
-//     and 669;
+//     and 669.  (It keeps 87 registers in memory, what it reads back between a
+//     tile's rows of results waits for their stores; 8192 x 8190 x 7168, whose
+//     last columns are cut: 281);
 //   128 x 256, from three quarters of the CUs on: 1500 x 4096 x 2048: 16.9 /
 //     14.9, 128 x 128: 21.7 / 17.1; at half (2048 x 2048 x 4096) 25.5 / 20.2 and
 //     21.3 / 15.8;
@@ -458,8 +463,8 @@ void launch_tiles(const MxProduct& p, int64_t tiles, int num_cu, hipStream_t str
 //     32: 81 / 66, 68 / 57 and 112 / 68;
 //   64 x 64 by four waves, from two to a CU on: 512 x 4096 x 4096: 17.2 / 13.6,
 //     by eight 19.7 / 15.5; 256 rows: 13.2 / 11.5 and 11.5 / 10.5.
-// Float results of E4M3 rows, whose operands take twice the registers and
-// products: 128 x 256 from four to a CU on (8192 x 4096 x 4096: 206, 64 x 256:
+// Float results of E4M3 rows, whose operands take twice the registers (128 x 256
+// keeps 13 in memory, read back for cut columns) and products: 128 x 256 from four to a CU on (8192 x 4096 x 4096: 206, 64 x 256:
 // 230; 2048 x 2048 x 4096: 52 and 33), 64 x 256 (that: 33, 32 x 128: 42), or 32
 // x 128 (1009 x 2002 x 5120: 27.7, 64 x 64: 31.2, 64 x 256: 37).
 template <bool A_FP4, bool SPLIT>

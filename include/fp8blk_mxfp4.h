@@ -131,8 +131,9 @@ int fp8_mxfp4_grouped_gemm(const uint8_t* a_q, const uint8_t* a_scale, int a_ele
  * a time and read the weights again for each.
  *
  * x [m x k] bf16 (16-byte aligned); q [n x k/2] (16-byte aligned); scale
- * [n x k/32]; y [m x n] out, bf16 or float per y_type (aligned to its
- * element).
+ * [n x k/32], at any address (the aligned dwords that its first and last bytes
+ * lie in are read whole); y [m x n] out, bf16 or float per y_type (aligned to
+ * its element).
  * Shape: 0 <= m < 2^31, 0 <= n <= 2^24, k % 32 == 0, 0 < k <= 2^24, m * k <
  *        2^30; m == 0 or n == 0 enqueues nothing.
  */
